@@ -294,6 +294,66 @@ jm_status jm_scan_bwd(const jm_dims* dims, const float* delta, const float* u, c
  * a NULL output, JM_ERR_UNSUPPORTED as jm_scan_bwd does. */
 jm_status jm_scan_bwd_schedule(const jm_dims* dims, int* n_parts);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a decoder block around the mixer: norm -> mixer -> residual ->
+ * norm -> feed-forward / mixture of experts -> residual (TransformerLens "Jamba"
+ * adapter page, "Architecture overview").  Conventions, ownership, streams and
+ * errors are those of the entry points above.  Matrices are row-major and packed
+ * unless a stride is named; every gradient has the type of what it is the
+ * gradient of.
+ * ------------------------------------------------------------------------- */
+
+/* JM_NORM_RMS: no mean subtraction, no bias.  JM_NORM_LAYER: LayerNorm. */
+enum { JM_NORM_RMS = 0, JM_NORM_LAYER = 1 };
+
+typedef struct {
+  int64_t rows;      /* >= 0 */
+  int64_t cols;      /* normalised width, 1..16384 (any value; multiples of 8 bf16 or 4
+                        float32 values are read 16 bytes at a time) */
+  int64_t x_stride;  /* elements from one row of x to the next, >= cols */
+  float eps;         /* inside the square root, >= 0 */
+  jm_dtype io;       /* type of every tensor except stats */
+  int32_t kind;      /* JM_NORM_RMS or JM_NORM_LAYER */
+  int32_t reserved;  /* must be 0 */
+} jm_norm_dims;
+
+/* Norm of each row, with the residual add before it:
+ *   s = x + residual (rounded to the io type; s = x without a residual)
+ *   y = (s - m) rstd weight + bias,  rstd = (mean((s - m)^2) + eps)^-1/2,
+ *   m = mean(s) for JM_NORM_LAYER, 0 for JM_NORM_RMS
+ *   x         in:  [rows, cols], rows x_stride elements apart
+ *   residual  in:  [rows, cols] or NULL
+ *   weight    in:  [cols];  bias in: [cols] or NULL (JM_NORM_LAYER only)
+ *   y         out: [rows, cols]
+ *   sum       out: [rows, cols], s; required with a residual, else NULL
+ *   stats     out: float32 [rows, 2], (m, rstd) of each row for jm_norm_bwd, or NULL
+ * y and sum may each be the same buffer as x (with x_stride == cols) or as the
+ * residual; any other overlap of an output with an input or with another output is
+ * refused with JM_ERR_INVALID_ARG. */
+jm_status jm_norm_fwd(const jm_norm_dims* dims, const void* x, const void* residual,
+                      const void* weight, const void* bias, void* y, void* sum, float* stats,
+                      jm_stream_t stream);
+
+/* Backward of jm_norm_fwd.  Given g_y = dLoss/dy and, where s is used again after
+ * the norm (a residual stream), g_sum = dLoss/ds from there:
+ *   g_x = rstd (g - [mean(g)] - xh mean(g xh)) + g_sum,  xh = (s - m) rstd,
+ *   g = g_y weight, the mean(g) term for JM_NORM_LAYER only;
+ *   g_weight = sum over rows of g_y xh,  g_bias = sum over rows of g_y.
+ *   x         in:  s, as jm_norm_fwd normalised it (its `sum`, or x), rows x_stride apart
+ *   stats     in:  float32 [rows, 2] from jm_norm_fwd
+ *   g_sum     in:  [rows, cols] or NULL
+ *   g_x       out: [rows, cols], the gradient of x and of the residual alike; may be the
+ *             same buffer as g_y or g_sum; any other overlap is refused
+ *   g_weight, g_bias out: [cols], each may be NULL; g_bias must be NULL for JM_NORM_RMS
+ * Sums are float32 in a fixed order: two runs give the same bits.  Workspace:
+ * jm_norm_bwd_workspace_size(dims) bytes, 256-byte aligned; its first 256 bytes
+ * are the error header jm_poll_error reads.  dims->eps is not read. */
+size_t jm_norm_bwd_workspace_size(const jm_norm_dims* dims);
+jm_status jm_norm_bwd(const jm_norm_dims* dims, const void* g_y, const void* x,
+                      const void* weight, const float* stats, const void* g_sum, void* g_x,
+                      void* g_weight, void* g_bias, void* workspace, size_t ws_bytes,
+                      jm_stream_t stream);
+
 /* Failure-detection self-test: launches one thread that waits, through the
  * same bounded wait the pipelines use, on a barrier that nothing completes.
  * The wait gives up after its limit (2 s), records site 99 in workspace's

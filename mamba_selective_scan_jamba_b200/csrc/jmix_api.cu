@@ -185,6 +185,16 @@ jm_status finish(Problem& p, cudaError_t e) {
 }
 
 }  // namespace
+
+void begin_call(Problem& p, jm_stream_t stream) {
+  memset(&p, 0, sizeof(p));
+  p.stream = reinterpret_cast<cudaStream_t>(stream);
+  p.events = g_events;
+  p.n_events = g_n_events;
+}
+
+jm_status finish_call(Problem& p, cudaError_t e) { return finish(p, e); }
+
 }  // namespace jmix
 
 namespace jmix {

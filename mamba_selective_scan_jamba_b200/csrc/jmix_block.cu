@@ -1,0 +1,221 @@
+// The C ABI of the decoder block's operators around the mixer (norms): host-side
+// validation, workspace sizing and dispatch.
+#include <string.h>
+
+#include "jmix_internal.cuh"
+
+#define JM_API extern "C" __attribute__((visibility("default")))
+
+namespace jmix {
+namespace {
+
+constexpr int64_t kMaxNormCols = 16384;
+
+// A named device pointer of a call, the bytes it covers and whether it is required.
+struct Arg {
+  const char* name;
+  const void* p;
+  size_t bytes;
+  bool required;
+};
+
+bool overlap(const Arg& a, const Arg& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+
+jm_status check_args(const Arg* args, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!args[i].p) {
+      if (!args[i].required) continue;
+      set_error("%s is NULL", args[i].name);
+      return JM_ERR_INVALID_ARG;
+    }
+    if (reinterpret_cast<uintptr_t>(args[i].p) % 16) {
+      set_error("%s is not 16-byte aligned", args[i].name);
+      return JM_ERR_INVALID_ARG;
+    }
+  }
+  return JM_OK;
+}
+
+jm_status refuse_overlap(const Arg& a, const Arg& b) {
+  set_error("%s overlaps %s", a.name, b.name);
+  return JM_ERR_INVALID_ARG;
+}
+
+jm_status check_workspace(const char* who, const void* ws, size_t given, size_t need) {
+  if (!ws) {
+    set_error("%s: workspace is NULL", who);
+    return JM_ERR_WORKSPACE;
+  }
+  if (reinterpret_cast<uintptr_t>(ws) % 256) {
+    set_error("%s: workspace must be 256-byte aligned", who);
+    return JM_ERR_WORKSPACE;
+  }
+  if (given < need) {
+    set_error("%s: workspace too small: %zu bytes given, %zu needed", who, given, need);
+    return JM_ERR_WORKSPACE;
+  }
+  return JM_OK;
+}
+
+jm_status check_norm_dims(const jm_norm_dims* d) {
+  if (!d) {
+    set_error("dims is NULL");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->io != JM_F32 && d->io != JM_BF16) {
+    set_error("io dtype must be JM_F32 or JM_BF16");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->kind != JM_NORM_RMS && d->kind != JM_NORM_LAYER) {
+    set_error("kind must be JM_NORM_RMS or JM_NORM_LAYER");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->reserved != 0) {
+    set_error("jm_norm_dims.reserved must be 0");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->rows < 0 || d->cols <= 0 || d->x_stride < d->cols) {
+    set_error("rows must be >= 0, cols > 0 and x_stride >= cols");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (!(d->eps >= 0.0f) || d->eps > 1e30f) {
+    set_error("eps must be finite and >= 0");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->cols > kMaxNormCols) {
+    set_error("cols > %lld is not built (got %lld)", (long long)kMaxNormCols, (long long)d->cols);
+    return JM_ERR_UNSUPPORTED;
+  }
+  if (d->rows > 0x7fffffffLL || (double)d->rows * (double)d->x_stride > 1.0e15) {
+    set_error("problem too large");
+    return JM_ERR_INVALID_ARG;
+  }
+  return JM_OK;
+}
+
+size_t esize(jm_dtype io) { return io == JM_BF16 ? 2 : 4; }
+
+size_t strided_bytes(const jm_norm_dims* d) {
+  return d->rows ? (size_t)((d->rows - 1) * d->x_stride + d->cols) * esize(d->io) : 0;
+}
+
+// The outputs may not overlap an input or one another, except that an output
+// named in `same` may be exactly that input's buffer (each value is read before
+// the thread that read it writes it).
+jm_status check_norm_overlap(const Arg* out, int n_out, const Arg* in, int n_in,
+                             const bool* same) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j) {
+      const bool ok = same[i * n_in + j] && out[i].p == in[j].p && out[i].bytes == in[j].bytes;
+      if (!ok && overlap(out[i], in[j])) return refuse_overlap(out[i], in[j]);
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return refuse_overlap(out[i], out[j]);
+  }
+  return JM_OK;
+}
+
+}  // namespace
+}  // namespace jmix
+
+using namespace jmix;
+
+JM_API jm_status jm_norm_fwd(const jm_norm_dims* dims, const void* x, const void* residual,
+                             const void* weight, const void* bias, void* y, void* sum,
+                             float* stats, jm_stream_t stream) {
+  jm_status st = check_norm_dims(dims);
+  if (st != JM_OK) return st;
+  const size_t es = esize(dims->io), act = (size_t)dims->rows * dims->cols * es,
+               vec = (size_t)dims->cols * es;
+  const bool any = dims->rows > 0;
+  if (bias && dims->kind == JM_NORM_RMS) {
+    set_error("bias must be NULL for JM_NORM_RMS");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (sum && !residual) {
+    set_error("sum must be NULL without a residual (it would be x)");
+    return JM_ERR_INVALID_ARG;
+  }
+  const Arg in[] = {{"x", x, strided_bytes(dims), any},
+                    {"residual", residual, act, false},
+                    {"weight", weight, vec, true},
+                    {"bias", bias, vec, false}};
+  const Arg out[] = {{"y", y, act, any},
+                     {"sum", sum, act, any && residual},
+                     {"stats", stats, (size_t)dims->rows * 8, false}};
+  if ((st = check_args(in, 4)) != JM_OK || (st = check_args(out, 3)) != JM_OK) return st;
+  const bool packed = dims->x_stride == dims->cols;
+  const bool same[] = {packed, true,  false, false,   // y
+                       packed, true,  false, false,   // sum
+                       false,  false, false, false};  // stats
+  if ((st = check_norm_overlap(out, 3, in, 4, same)) != JM_OK) return st;
+  Problem p;
+  begin_call(p, stream);
+  if (!any) return finish_call(p, cudaSuccess);
+  NormFwdArgs a{};
+  a.rows = dims->rows;
+  a.cols = dims->cols;
+  a.x_stride = dims->x_stride;
+  a.eps = dims->eps;
+  a.layer = dims->kind == JM_NORM_LAYER;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.bias = bias;
+  a.y = y;
+  a.sum = sum;
+  a.stats = stats;
+  return finish_call(p, run_norm_fwd(a, dims->io, p));
+}
+
+JM_API size_t jm_norm_bwd_workspace_size(const jm_norm_dims* dims) {
+  if (check_norm_dims(dims) != JM_OK) return 0;
+  return norm_bwd_ws_bytes(dims->rows, dims->cols, dims->x_stride, dims->io);
+}
+
+JM_API jm_status jm_norm_bwd(const jm_norm_dims* dims, const void* g_y, const void* x,
+                             const void* weight, const float* stats, const void* g_sum, void* g_x,
+                             void* g_weight, void* g_bias, void* workspace, size_t ws_bytes,
+                             jm_stream_t stream) {
+  jm_status st = check_norm_dims(dims);
+  if (st != JM_OK) return st;
+  const size_t es = esize(dims->io), act = (size_t)dims->rows * dims->cols * es,
+               vec = (size_t)dims->cols * es;
+  const bool any = dims->rows > 0;
+  if (g_bias && dims->kind == JM_NORM_RMS) {
+    set_error("g_bias must be NULL for JM_NORM_RMS");
+    return JM_ERR_INVALID_ARG;
+  }
+  const size_t need = jm_norm_bwd_workspace_size(dims);
+  const Arg in[] = {{"g_y", g_y, act, any},
+                    {"x", x, strided_bytes(dims), any},
+                    {"weight", weight, vec, true},
+                    {"stats", stats, (size_t)dims->rows * 8, any},
+                    {"g_sum", g_sum, act, false}};
+  const Arg out[] = {{"g_x", g_x, act, any},
+                     {"g_weight", g_weight, vec, false},
+                     {"g_bias", g_bias, vec, false},
+                     {"workspace", workspace, need, false}};
+  if ((st = check_args(in, 5)) != JM_OK || (st = check_args(out, 3)) != JM_OK) return st;
+  if ((st = check_workspace("jm_norm_bwd", workspace, ws_bytes, need)) != JM_OK) return st;
+  const bool same[20] = {true, false, false, false, true};  // g_x: g_y or g_sum
+  if ((st = check_norm_overlap(out, 4, in, 5, same)) != JM_OK) return st;
+  Problem p;
+  begin_call(p, stream);
+  NormBwdArgs a{};
+  a.rows = dims->rows;
+  a.cols = dims->cols;
+  a.x_stride = dims->x_stride;
+  a.layer = dims->kind == JM_NORM_LAYER;
+  a.gy = g_y;
+  a.x = x;
+  a.weight = weight;
+  a.stats = stats;
+  a.g_sum = g_sum;
+  a.g_x = g_x;
+  return finish_call(p, run_norm_bwd(a, g_weight, g_bias, static_cast<char*>(workspace), dims->io,
+                                     p));
+}

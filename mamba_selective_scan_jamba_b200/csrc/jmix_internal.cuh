@@ -96,6 +96,43 @@ cudaError_t gemm_bf16_tn(int64_t M, int64_t N, int64_t K, const void* A, const v
                          void* C0, void* C1, int64_t n_split, ErrFlags* err,
                          const ErrFlags* fold, cudaStream_t s, bool pdl);
 
+// The norms of k_norm.cu.  wpr (warps per row) and rpc (rows per CTA) are filled
+// in by the launcher.
+struct NormFwdArgs {
+  int64_t rows, cols, x_stride;
+  float eps;
+  bool layer;            // LayerNorm (else RMSNorm)
+  const void* x;
+  const void* residual;  // may be null
+  const void* weight;
+  const void* bias;      // may be null
+  void* y;
+  void* sum;             // x + residual (null without a residual)
+  float* stats;          // [rows][mean, rstd], may be null
+  int wpr, rpc;
+};
+struct NormBwdArgs {
+  int64_t rows, cols, x_stride;
+  bool layer;
+  const void* gy;
+  const void* x;
+  const void* weight;
+  const float* stats;
+  const void* g_sum;     // may be null
+  void* g_x;
+  float* part;           // partial rows of g_w and g_b, or null
+  ErrFlags* err;
+  int wpr, rpc;
+};
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t x_stride, jm_dtype io);
+cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p);
+cudaError_t run_norm_bwd(NormBwdArgs a, void* g_w, void* g_b, char* ws, jm_dtype io, Problem& p);
+
+// Launch accounting of a call outside the mixer: an empty Problem on `stream`
+// with this thread's timing events, and the status of its end.
+void begin_call(Problem& p, jm_stream_t stream);
+jm_status finish_call(Problem& p, cudaError_t e);
+
 // Per-thread message for jm_last_error.
 void set_error(const char* fmt, ...);
 

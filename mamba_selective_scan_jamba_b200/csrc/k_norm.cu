@@ -1,0 +1,468 @@
+// LayerNorm / RMSNorm over the rows of a matrix, with the residual add before
+// it, and its backward with the weight's and bias's gradients.
+//
+//   s    = x + r, rounded to the io type (the value the residual stream carries)
+//   y    = (s - m) rstd w + b,  rstd = (mean((s - m)^2) + eps)^-1/2,
+//          m = mean(s) (LayerNorm) or 0 (RMSNorm)
+//   xh   = (s - m) rstd,  g = gy w
+//   g_x  = rstd (g - [mean(g)] - xh mean(g xh)) + g_sum
+//   g_w  = sum over rows of gy xh,  g_b = sum over rows of gy
+//
+// Both passes are bound by HBM: a row is read once into registers and every
+// statistic is taken from there, so the forward moves 2 (4 with a residual) and
+// the backward 3 (4) values per element.  The variance is the mean of the squared
+// differences from the mean (two reductions over registers), not E[s^2] - m^2,
+// which cancels for rows far from zero.  All arithmetic is float32; y, sum and
+// the gradients are rounded once to the io type.
+//
+// A group of `wpr` warps owns a row; a thread keeps NV vectors of VEC values
+// (16-byte accesses; VEC = 1 where the width or the stride is not a multiple of
+// 16 bytes).  In the backward a group walks over rows with a stride, so that each
+// thread owns its columns of g_w and g_b and sums them in registers; the groups'
+// partial rows go to the workspace and k_norm_bwd_reduce adds them in a fixed
+// order (the same bits on every run).
+#include "jmix_internal.cuh"
+#include "sm100.cuh"
+
+namespace jmix {
+namespace {
+
+using sm100::grid_dep_launch;
+using sm100::grid_dep_wait;
+
+constexpr int kNormSMs = 148;
+
+template <typename T, int VEC>
+struct RawT {
+  using type = uint4;
+};
+template <typename T>
+struct RawT<T, 1> {
+  using type = T;
+};
+template <typename T, int VEC>
+using Raw = typename RawT<T, VEC>::type;
+
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Raw<T, VEC>& r, float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    f[0] = static_cast<float>(r);
+  } else if constexpr (sizeof(T) == 4) {
+    f[0] = __uint_as_float(r.x);
+    f[1] = __uint_as_float(r.y);
+    f[2] = __uint_as_float(r.z);
+    f[3] = __uint_as_float(r.w);
+  } else {
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> pack(const float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    return static_cast<T>(f[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  } else {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+template <typename R>
+__device__ __forceinline__ R zero_raw() {
+  if constexpr (sizeof(R) == 16)
+    return make_uint4(0u, 0u, 0u, 0u);
+  else
+    return static_cast<R>(0.0f);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sums over the group's threads (every thread of the CTA calls it together;
+// `red` holds one value per warp of the CTA and is not reused before the next
+// barrier of the caller).
+__device__ __forceinline__ float group_sum(float v, float* red, int wpr) {
+  v = warp_sum(v);
+  if (wpr == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  const int first = warp / wpr * wpr;
+  return warp_sum(lane < wpr ? red[first + lane] : 0.0f);
+}
+
+template <typename T, int VEC, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_norm_fwd(const NormFwdArgs a) {
+  __shared__ float red[2][32];
+  using R = Raw<T, VEC>;
+  const int gthreads = 32 * a.wpr;
+  const int group = threadIdx.x / gthreads, t = threadIdx.x - group * gthreads;
+  const int64_t row = (int64_t)blockIdx.x * a.rpc + group;
+  const bool live = row < a.rows;
+  const int nvec = (int)(a.cols / VEC);
+  grid_dep_wait();
+  const R* x = reinterpret_cast<const R*>(static_cast<const T*>(a.x) + (live ? row : 0) * a.x_stride);
+  const int64_t base = (live ? row : 0) * (int64_t)nvec;
+  const R* res = a.residual ? static_cast<const R*>(a.residual) + base : nullptr;
+  const R* wp = static_cast<const R*>(a.weight);
+  const R* bp = static_cast<const R*>(a.bias);
+  R rx[NV], rr[NV], rw[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = v * gthreads + t;
+    const bool ok = live && i < nvec;
+    rx[v] = ok ? x[i] : zero_raw<R>();
+    if (res) rr[v] = ok ? res[i] : zero_raw<R>();
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = v * gthreads + t;
+    rw[v] = i < nvec ? wp[i] : zero_raw<R>();
+  }
+  float s[NV][VEC];
+  float acc = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    unpack<T, VEC>(rx[v], s[v]);
+    if (res) {
+      float q[VEC];
+      unpack<T, VEC>(rr[v], q);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s[v][j] += q[j];
+      // the normalised value is the stored one, so that the backward, which
+      // reads `sum`, differentiates what was computed here
+      const R p = pack<T, VEC>(s[v]);
+      unpack<T, VEC>(p, s[v]);
+      const int i = v * gthreads + t;
+      if (live && i < nvec) (static_cast<R*>(a.sum) + base)[i] = p;
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc += a.layer ? s[v][j] : s[v][j] * s[v][j];
+  }
+  const float inv_n = 1.0f / (float)a.cols;
+  float mean = 0.0f, var;
+  if (a.layer) {
+    mean = group_sum(acc, red[0], a.wpr) * inv_n;
+    acc = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (v * gthreads + t < nvec)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc = fmaf(s[v][j] - mean, s[v][j] - mean, acc);
+    var = group_sum(acc, red[1], a.wpr) * inv_n;
+  } else {
+    var = group_sum(acc, red[0], a.wpr) * inv_n;
+  }
+  const float rstd = 1.0f / sqrtf(var + a.eps);
+  if (!live) return;
+  R* y = static_cast<R*>(a.y) + base;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = v * gthreads + t;
+    if (i >= nvec) break;
+    float w[VEC], o[VEC];
+    unpack<T, VEC>(rw[v], w);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] = (s[v][j] - mean) * rstd * w[j];
+    if (bp) {
+      float b[VEC];
+      unpack<T, VEC>(bp[i], b);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[j] += b[j];
+    }
+    y[i] = pack<T, VEC>(o);
+  }
+  if (a.stats && t == 0) {
+    a.stats[2 * row] = mean;
+    a.stats[2 * row + 1] = rstd;
+  }
+}
+
+template <typename T, int VEC, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) k_norm_bwd(const NormBwdArgs a) {
+  __shared__ float red[2][2][32];
+  using R = Raw<T, VEC>;
+  const int gthreads = 32 * a.wpr;
+  const int group = threadIdx.x / gthreads, t = threadIdx.x - group * gthreads;
+  const int nvec = (int)(a.cols / VEC);
+  const int64_t step = (int64_t)gridDim.x * a.rpc;
+  const int64_t first = (int64_t)blockIdx.x * a.rpc + group;
+  grid_dep_wait();
+  if (blockIdx.x == 0 && threadIdx.x < sizeof(ErrFlags) / 4)
+    reinterpret_cast<unsigned*>(a.err)[threadIdx.x] = 0u;
+  const R* wp = static_cast<const R*>(a.weight);
+  R rw[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = v * gthreads + t;
+    rw[v] = i < nvec ? wp[i] : zero_raw<R>();
+  }
+  float gw[NV][VEC], gb[NV][VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) gw[v][j] = gb[v][j] = 0.0f;
+  const float inv_n = 1.0f / (float)a.cols;
+
+  R rx[NV], rg[NV];
+  float mean = 0.0f, rstd = 0.0f;
+  auto load = [&](int64_t row) {
+    const bool live = row < a.rows;
+    const R* x = reinterpret_cast<const R*>(static_cast<const T*>(a.x) + (live ? row : 0) * a.x_stride);
+    const R* g = static_cast<const R*>(a.gy) + (live ? row : 0) * (int64_t)nvec;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = v * gthreads + t;
+      const bool ok = live && i < nvec;
+      rx[v] = ok ? x[i] : zero_raw<R>();
+      rg[v] = ok ? g[i] : zero_raw<R>();
+    }
+    mean = live ? a.stats[2 * row] : 0.0f;
+    rstd = live ? a.stats[2 * row + 1] : 0.0f;
+  };
+  load(first);
+  // every group of the CTA runs the same number of rounds (barriers inside)
+  const int64_t rounds = (a.rows - (int64_t)blockIdx.x * a.rpc + step - 1) / step;
+  for (int64_t it = 0; it < rounds; ++it) {
+    const int64_t row = first + it * step;
+    const bool live = row < a.rows;
+    const int64_t base = (live ? row : 0) * (int64_t)nvec;
+    float xh[NV][VEC], g[NV][VEC];
+    float sg = 0.0f, sgx = 0.0f;
+    const float rs = rstd;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float w[VEC];
+      unpack<T, VEC>(rx[v], xh[v]);
+      unpack<T, VEC>(rg[v], g[v]);
+      unpack<T, VEC>(rw[v], w);
+      const bool in = live && v * gthreads + t < nvec;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        xh[v][j] = in ? (xh[v][j] - mean) * rs : 0.0f;
+        gw[v][j] = fmaf(g[v][j], xh[v][j], gw[v][j]);
+        gb[v][j] += g[v][j];
+        g[v][j] *= w[j];
+        sg += g[v][j];
+        sgx = fmaf(g[v][j], xh[v][j], sgx);
+      }
+    }
+    load(row + step);  // in flight during this row's reductions
+    sg = warp_sum(sg);
+    sgx = warp_sum(sgx);
+    if (a.wpr > 1) {
+      float(*rd)[32] = red[it & 1];
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+      if (lane == 0) {
+        rd[0][warp] = sg;
+        rd[1][warp] = sgx;
+      }
+      __syncthreads();
+      const int w0 = warp / a.wpr * a.wpr;
+      sg = warp_sum(lane < a.wpr ? rd[0][w0 + lane] : 0.0f);
+      sgx = warp_sum(lane < a.wpr ? rd[1][w0 + lane] : 0.0f);
+    }
+    const float c0 = a.layer ? sg * inv_n : 0.0f, c1 = sgx * inv_n;
+    if (live) {
+      const R* gs = a.g_sum ? static_cast<const R*>(a.g_sum) + base : nullptr;
+      R* gx = static_cast<R*>(a.g_x) + base;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int i = v * gthreads + t;
+        if (i >= nvec) break;
+        float o[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o[j] = (g[v][j] - c0 - xh[v][j] * c1) * rs;
+        if (gs) {
+          float q[VEC];
+          unpack<T, VEC>(gs[i], q);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) o[j] += q[j];
+        }
+        gx[i] = pack<T, VEC>(o);
+      }
+    }
+  }
+  if (a.part) {
+    float* pw = a.part + ((int64_t)blockIdx.x * a.rpc + group) * 2 * a.cols;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = v * gthreads + t;
+      if (i >= nvec) break;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        pw[(int64_t)i * VEC + j] = gw[v][j];
+        pw[a.cols + (int64_t)i * VEC + j] = gb[v][j];
+      }
+    }
+  }
+  grid_dep_launch();
+}
+
+// g_w (blockIdx.y = 0) and g_b (1): the partial rows of 32 columns, added in a
+// fixed order.
+constexpr int kRedRows = 16;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kRedRows)
+    k_norm_bwd_reduce(const float* __restrict__ part, int64_t n_part, int64_t cols, T* g_w,
+                      T* g_b) {
+  __shared__ float sh[kRedRows][33];
+  T* out = blockIdx.y == 0 ? g_w : g_b;
+  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  grid_dep_wait();
+  if (!out) return;
+  float acc = 0.0f;
+  if (c < cols) {
+    const float* p = part + blockIdx.y * cols + c;
+    for (int64_t r = threadIdx.y; r < n_part; r += kRedRows) acc += p[r * 2 * cols];
+  }
+  sh[threadIdx.y][threadIdx.x] = acc;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < kRedRows; ++i) acc += sh[i][threadIdx.x];
+    out[c] = static_cast<T>(acc);
+  }
+}
+
+// How a row is laid over threads: the vector width, vectors per thread, warps
+// per row and rows per CTA.
+struct NormShape {
+  int vec, nv, wpr, rpc;
+  int threads() const { return 32 * wpr * rpc; }
+};
+
+NormShape norm_shape(int64_t cols, int64_t x_stride, jm_dtype io) {
+  NormShape s;
+  const int full = io == JM_BF16 ? 8 : 4;
+  s.vec = cols % full == 0 && x_stride % full == 0 ? full : 1;
+  const int64_t nvec = cols / s.vec;
+  // the fewest warps that hold the row at 2 (scalar: 4) vectors a thread, and
+  // more vectors a thread only where 32 warps are not enough
+  s.nv = s.vec > 1 ? 2 : 4;
+  s.wpr = 1;
+  while (s.wpr < 32 && (int64_t)32 * s.wpr * s.nv < nvec) s.wpr *= 2;
+  if ((int64_t)32 * s.wpr * s.nv < nvec) s.nv = s.vec > 1 ? 4 : 16;
+  s.rpc = s.wpr >= 8 ? 1 : 8 / s.wpr;  // CTAs of 256 threads, or one wider row
+  return s;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t s,
+                       Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename Args>
+using NormKern = void (*)(const Args);
+
+// The kernel built for a shape's threads (rounded up to 256, 512 or 1024, which
+// sets the registers a thread may use).  16,384 columns need 4 vectors a thread
+// only in float32 and 16 values only in scalar form, both at 1024 threads.
+#define JMIX_NORM_PICK(KERN, T, FULL)                                                   \
+  (s.vec > 1 ? (s.nv == 4             ? KERN<T, FULL, 16 / FULL, 1024>                  \
+                : s.threads() <= 256  ? KERN<T, FULL, 2, 256>                           \
+                : s.threads() <= 512  ? KERN<T, FULL, 2, 512>                           \
+                                      : KERN<T, FULL, 2, 1024>)                         \
+             : (s.nv == 16            ? KERN<T, 1, 16, 1024>                            \
+                : s.threads() <= 256  ? KERN<T, 1, 4, 256>                              \
+                : s.threads() <= 512  ? KERN<T, 1, 4, 512>                              \
+                                      : KERN<T, 1, 4, 1024>))
+
+NormKern<NormFwdArgs> fwd_kernel(const NormShape& s, jm_dtype io) {
+  if (io == JM_BF16) return JMIX_NORM_PICK(k_norm_fwd, __nv_bfloat16, 8);
+  return JMIX_NORM_PICK(k_norm_fwd, float, 4);
+}
+
+NormKern<NormBwdArgs> bwd_kernel(const NormShape& s, jm_dtype io) {
+  if (io == JM_BF16) return JMIX_NORM_PICK(k_norm_bwd, __nv_bfloat16, 8);
+  return JMIX_NORM_PICK(k_norm_bwd, float, 4);
+}
+#undef JMIX_NORM_PICK
+
+// CTAs of the backward: as many as are resident at once, so that there are few
+// partial rows to add.
+int64_t bwd_ctas(int64_t rows, const NormShape& s) {
+  const int64_t most = (int64_t)kNormSMs * (s.threads() <= 256 ? 3 : 1);
+  const int64_t need = (rows + s.rpc - 1) / s.rpc;
+  return need < most ? need : most;
+}
+
+}  // namespace
+
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t x_stride, jm_dtype io) {
+  const NormShape s = norm_shape(cols, x_stride, io);
+  return sizeof(ErrFlags) + align256((size_t)(bwd_ctas(rows, s) * s.rpc * 2 * cols) * 4);
+}
+
+cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p) {
+  const NormShape s = norm_shape(a.cols, a.x_stride, io);
+  a.wpr = s.wpr;
+  a.rpc = s.rpc;
+  const int64_t ctas = (a.rows + s.rpc - 1) / s.rpc;
+    launches_begin(p);
+  const cudaError_t e = launch_pdl(fwd_kernel(s, io), dim3((unsigned)ctas), dim3(s.threads()),
+                                   p.stream, a);
+  if (e == cudaSuccess) launched(p, "k_norm_fwd");
+  return e;
+}
+
+cudaError_t run_norm_bwd(NormBwdArgs a, void* g_w, void* g_b, char* ws, jm_dtype io, Problem& p) {
+  const NormShape s = norm_shape(a.cols, a.x_stride, io);
+  a.wpr = s.wpr;
+  a.rpc = s.rpc;
+  a.err = reinterpret_cast<ErrFlags*>(ws);
+  const bool sums = g_w || g_b;
+  float* part = reinterpret_cast<float*>(ws + sizeof(ErrFlags));
+  a.part = sums ? part : nullptr;
+  const int64_t ctas = bwd_ctas(a.rows, s);
+  cudaError_t e = cudaSuccess;
+  launches_begin(p);
+  if (ctas > 0) {
+    e = launch_pdl(bwd_kernel(s, io), dim3((unsigned)ctas), dim3(s.threads()), p.stream, a);
+    if (e == cudaSuccess) launched(p, "k_norm_bwd");
+  } else {
+    e = cudaMemsetAsync(ws, 0, sizeof(ErrFlags), p.stream);
+  }
+  if (e == cudaSuccess && sums) {
+    const dim3 grid((unsigned)((a.cols + 31) / 32), 2);
+    if (io == JM_BF16)
+      e = launch_pdl(k_norm_bwd_reduce<__nv_bfloat16>, grid, dim3(32, kRedRows), p.stream,
+                     (const float*)part, ctas * s.rpc, a.cols, static_cast<__nv_bfloat16*>(g_w),
+                     static_cast<__nv_bfloat16*>(g_b));
+    else
+      e = launch_pdl(k_norm_bwd_reduce<float>, grid, dim3(32, kRedRows), p.stream,
+                     (const float*)part, ctas * s.rpc, a.cols, static_cast<float*>(g_w),
+                     static_cast<float*>(g_b));
+    if (e == cudaSuccess) launched(p, "k_norm_bwd_reduce");
+  }
+  return e;
+}
+
+}  // namespace jmix

@@ -30,7 +30,7 @@ EXPORTED = ("jm_mixer_fwd_workspace_size", "jm_mixer_step_workspace_size", "jm_m
             "jm_layer_fwd_workspace_size", "jm_layer_fwd", "jm_scan_bwd_workspace_size",
             "jm_scan_bwd", "jm_scan_bwd_schedule", "jm_noalloc_poll_error",
             "jm_noalloc_selftest_timeout", "jm_prepared_weights_size", "jm_prepare_weights",
-            "jm_mixer_step_indexed")
+            "jm_mixer_step_indexed", "jm_norm_fwd", "jm_norm_bwd_workspace_size", "jm_norm_bwd")
 
 
 class jm_dims(ctypes.Structure):
@@ -39,6 +39,12 @@ class jm_dims(ctypes.Structure):
                 ("d_conv", ctypes.c_int64), ("dt_rank", ctypes.c_int64),
                 ("eps", ctypes.c_float), ("io", ctypes.c_int),
                 ("discretization", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class jm_norm_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("io", ctypes.c_int), ("kind", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class JmixError(RuntimeError):
@@ -103,6 +109,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.jm_mixer_step_indexed.restype = ctypes.c_int
     lib.jm_mixer_step_indexed.argtypes = ([ctypes.POINTER(jm_dims), _vp, ctypes.c_int64]
                                           + [_vp] * 14 + [_vp, _vp, _vp, ctypes.c_size_t, _vp])
+    lib.jm_norm_fwd.restype = ctypes.c_int
+    lib.jm_norm_fwd.argtypes = [ctypes.POINTER(jm_norm_dims)] + [_vp] * 8
+    lib.jm_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.jm_norm_bwd_workspace_size.argtypes = [ctypes.POINTER(jm_norm_dims)]
+    lib.jm_norm_bwd.restype = ctypes.c_int
+    lib.jm_norm_bwd.argtypes = ([ctypes.POINTER(jm_norm_dims)] + [_vp] * 9
+                                + [ctypes.c_size_t, _vp])
     lib.jm_noalloc_poll_error.restype = ctypes.c_int
     lib.jm_noalloc_poll_error.argtypes = [_vp]
     lib.jm_noalloc_selftest_timeout.restype = ctypes.c_int
@@ -127,6 +140,14 @@ def dims(batch: int, seqlen: int, d_inner: int, dt_rank: int, io: int = JM_BF16,
          eps: float = 1e-6, d_state: int = 16, d_conv: int = 4, zoh: bool = False) -> jm_dims:
     return jm_dims(batch, seqlen, d_inner, d_state, d_conv, dt_rank, eps, io,
                    JM_DISC_ZOH if zoh else JM_DISC_EULER, 0)
+
+
+JM_NORM_RMS, JM_NORM_LAYER = 0, 1
+
+
+def norm_dims(rows: int, cols: int, io: int = JM_BF16, kind: int = JM_NORM_RMS,
+              eps: float = 1e-6, x_stride: Optional[int] = None) -> jm_norm_dims:
+    return jm_norm_dims(rows, cols, cols if x_stride is None else x_stride, eps, io, kind, 0)
 
 
 def _ptr(t) -> Optional[int]:
@@ -217,6 +238,63 @@ def jm_scan_bwd(d: jm_dims, delta, u, Bm, Cm, A_log, D, h0, gy, g_delta, g_u, g_
     st = load().jm_scan_bwd(ctypes.byref(d), *[_ptr(t) for t in (
         delta, u, Bm, Cm, A_log, D, h0, gy, g_delta, g_u, g_B, g_C, g_A_log, g_D, g_h0,
         workspace)], ws_bytes, _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def _tensors(io: int, **named):
+    """Addresses of the named tensors.  A torch tensor's layout and type cannot be read
+    from its address, so they are checked here: on the current device, of the call's io
+    type (names ending in ``_f32`` float32, in ``_i32`` int32), contiguous (names ending in
+    ``_rows``: contiguous within a row; its stride is the dims' business)."""
+    out = []
+    for name, t in named.items():
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        import torch
+        want = torch.bfloat16 if io == JM_BF16 else torch.float32
+        ok = t.is_contiguous()
+        base, _, tag = name.rpartition("_")
+        if tag == "f32":
+            name, want = base, torch.float32
+        elif tag == "i32":
+            name, want = base, torch.int32
+        elif tag == "rows":
+            name, ok = base, t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1
+        if t.dtype != want:
+            raise JmixError(JM_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call needs {want}")
+        if not ok:
+            raise JmixError(JM_ERR_INVALID_ARG, f"{name} is not contiguous")
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise JmixError(JM_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current "
+                                                "CUDA device")
+        out.append(t.data_ptr())
+    return out
+
+
+def jm_norm_fwd(d: jm_norm_dims, x, weight, y, bias=None, residual=None, sum_out=None, stats=None,
+                stream=None, check: bool = True) -> int:
+    """Residual add and LayerNorm / RMSNorm of each row (see include/jmix.h)."""
+    p = _tensors(d.io, x_rows=x, residual=residual, weight=weight, bias=bias, y=y, sum=sum_out,
+                 stats_f32=stats)
+    st = load().jm_norm_fwd(ctypes.byref(d), *p, _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def jm_norm_bwd_workspace_size(d: jm_norm_dims) -> int:
+    return load().jm_norm_bwd_workspace_size(ctypes.byref(d))
+
+
+def jm_norm_bwd(d: jm_norm_dims, g_y, x, weight, stats, g_x, workspace, ws_bytes: int, g_sum=None,
+                g_weight=None, g_bias=None, stream=None, check: bool = True) -> int:
+    """Backward of jm_norm_fwd (see include/jmix.h); x is the forward's sum, or its x."""
+    p = _tensors(d.io, g_y=g_y, x_rows=x, weight=weight, stats_f32=stats, g_sum=g_sum, g_x=g_x,
+                 g_weight=g_weight, g_bias=g_bias)
+    st = load().jm_norm_bwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
     if check:
         _check(st)
     return st

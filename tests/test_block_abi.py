@@ -1,0 +1,110 @@
+"""CPU checks of the decoder block's operators: the host refuses bad arguments
+before any launch (no call below reaches the GPU)."""
+import pytest
+
+from mamba_selective_scan_jamba_b200 import build, jmix
+
+F = 1 << 40        # fake, never dereferenced device addresses, far apart
+G = 1 << 36
+W = 1 << 45        # fake workspace
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build_libjmix()
+    return jmix.load()
+
+
+def norm_fwd(d, **over):
+    a = dict(x=F, weight=F + 2 * G, y=F + 3 * G, bias=None, residual=None, sum_out=None, stats=None)
+    a.update(over)
+    return jmix.jm_norm_fwd(d, **a, stream=0, check=False)
+
+
+def norm_bwd(d, nbytes=None, **over):
+    a = dict(g_y=F, x=F + G, weight=F + 2 * G, stats=F + 3 * G, g_x=F + 4 * G, workspace=W,
+             ws_bytes=jmix.jm_norm_bwd_workspace_size(d) if nbytes is None else nbytes)
+    a.update(over)
+    return jmix.jm_norm_bwd(d, **a, stream=0, check=False)
+
+
+@pytest.mark.parametrize("over,code,msg", [
+    (dict(rows=-1), jmix.JM_ERR_INVALID_ARG, "rows"),
+    (dict(cols=0), jmix.JM_ERR_INVALID_ARG, "cols"),
+    (dict(x_stride=31), jmix.JM_ERR_INVALID_ARG, "x_stride"),
+    (dict(cols=16385), jmix.JM_ERR_UNSUPPORTED, "16384"),
+    (dict(rows=1 << 32), jmix.JM_ERR_INVALID_ARG, "large"),
+    (dict(eps=-1.0), jmix.JM_ERR_INVALID_ARG, "eps"),
+    (dict(eps=float("nan")), jmix.JM_ERR_INVALID_ARG, "eps"),
+    (dict(io=5), jmix.JM_ERR_INVALID_ARG, "io dtype"),
+    (dict(kind=2), jmix.JM_ERR_INVALID_ARG, "kind"),
+])
+def test_norm_rejects_bad_dims(over, code, msg):
+    kw = dict(rows=4, cols=32)
+    kw.update(over)
+    d = jmix.norm_dims(**kw)
+    assert norm_fwd(d) == code and msg in jmix.jm_last_error()
+    assert norm_bwd(d, nbytes=1 << 20) == code and msg in jmix.jm_last_error()
+    assert jmix.jm_norm_bwd_workspace_size(d) == 0
+    d = jmix.norm_dims(4, 32)
+    d.reserved = 1
+    assert norm_fwd(d) == jmix.JM_ERR_INVALID_ARG and "reserved" in jmix.jm_last_error()
+
+
+def test_norm_rejects_bad_pointers():
+    d = jmix.norm_dims(4, 32, kind=jmix.JM_NORM_LAYER)
+    bad = jmix.JM_ERR_INVALID_ARG
+    for k in ("x", "weight", "y"):
+        assert norm_fwd(d, **{k: None}) == bad and "NULL" in jmix.jm_last_error(), k
+        assert norm_fwd(d, **{k: F + 8}) == bad and "aligned" in jmix.jm_last_error(), k
+    assert norm_fwd(d, residual=F + 5 * G) == bad and "sum is NULL" in jmix.jm_last_error()
+    assert norm_fwd(d, sum_out=F + 5 * G) == bad and "without a residual" in jmix.jm_last_error()
+    # y over the weight, half over x, over the sum; sum half over the residual
+    assert norm_fwd(d, y=F + 2 * G) == bad and "y overlaps weight" in jmix.jm_last_error()
+    assert norm_fwd(d, y=F + 64) == bad and "y overlaps x" in jmix.jm_last_error()
+    r = F + 5 * G
+    assert norm_fwd(d, residual=r, sum_out=F + 3 * G) == bad
+    assert "sum overlaps y" in jmix.jm_last_error()
+    assert norm_fwd(d, residual=r, sum_out=r + 16) == bad
+    assert "sum overlaps residual" in jmix.jm_last_error()
+    assert norm_fwd(d, stats=F) == bad and "stats overlaps x" in jmix.jm_last_error()
+    strided = jmix.norm_dims(4, 32, kind=jmix.JM_NORM_LAYER, x_stride=40)
+    assert norm_fwd(strided, y=F) == bad and "y overlaps x" in jmix.jm_last_error()
+    rms = jmix.norm_dims(4, 32)
+    assert norm_fwd(rms, bias=F + G) == bad and "bias" in jmix.jm_last_error()
+
+
+def test_norm_bwd_rejects_bad_pointers():
+    d = jmix.norm_dims(4, 32)
+    bad = jmix.JM_ERR_INVALID_ARG
+    for k in ("g_y", "x", "weight", "stats", "g_x"):
+        assert norm_bwd(d, **{k: None}) == bad and "NULL" in jmix.jm_last_error(), k
+    assert norm_bwd(d, g_x=F + G) == bad and "g_x overlaps x" in jmix.jm_last_error()
+    assert norm_bwd(d, g_x=F + 16) == bad and "g_x overlaps g_y" in jmix.jm_last_error()
+    assert norm_bwd(d, g_weight=F + 2 * G) == bad
+    assert norm_bwd(d, g_bias=F + 6 * G) == bad and "g_bias" in jmix.jm_last_error()
+    n = jmix.jm_norm_bwd_workspace_size(d)
+    assert norm_bwd(d, nbytes=n - 1) == jmix.JM_ERR_WORKSPACE
+    assert norm_bwd(d, workspace=None) == jmix.JM_ERR_WORKSPACE
+    assert norm_bwd(d, workspace=W + 16) == jmix.JM_ERR_WORKSPACE
+    assert norm_bwd(d, workspace=F + G) == bad and "workspace overlaps x" in jmix.jm_last_error()
+
+
+def test_norm_no_rows_needs_no_buffers():
+    assert norm_fwd(jmix.norm_dims(0, 32), x=None, y=None) == jmix.JM_OK
+    assert jmix.jm_last_launch_count() == 0
+
+
+def test_binding_checks_tensors():
+    """What an address cannot say is checked in the binding."""
+    import torch
+    t = torch.zeros(4, 32, dtype=torch.bfloat16)
+    with pytest.raises(jmix.JmixError, match="x is torch.bfloat16") as e:
+        jmix.jm_norm_fwd(jmix.norm_dims(4, 32, io=jmix.JM_F32), t, F, F, stream=0)
+    assert e.value.status == jmix.JM_ERR_INVALID_ARG
+    with pytest.raises(jmix.JmixError, match="residual is not contiguous"):
+        jmix.jm_norm_fwd(jmix.norm_dims(4, 32), F, F, F, residual=t.t(), stream=0)
+    with pytest.raises(jmix.JmixError, match="stats is torch.bfloat16"):
+        jmix.jm_norm_fwd(jmix.norm_dims(4, 32), F, F, F, stats=t, stream=0)
+    with pytest.raises(jmix.JmixError, match="CUDA device"):
+        jmix.jm_norm_fwd(jmix.norm_dims(4, 32), t, F, F, stream=0)
