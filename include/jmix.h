@@ -354,6 +354,48 @@ jm_status jm_norm_bwd(const jm_norm_dims* dims, const void* g_y, const void* x,
                       void* g_weight, void* g_bias, void* workspace, size_t ws_bytes,
                       jm_stream_t stream);
 
+/* Activation of jm_linear_fwd: GELU is v Phi(v) (the exact, erf form). */
+enum { JM_ACT_NONE = 0, JM_ACT_RELU = 1, JM_ACT_GELU = 2, JM_ACT_SILU = 3 };
+
+typedef struct {
+  int64_t rows;          /* tokens, >= 0 (any value) */
+  int64_t in_features;   /* positive multiple of 8 */
+  int64_t out_features;  /* positive multiple of 8 */
+  jm_dtype io;           /* JM_BF16 (JM_ERR_UNSUPPORTED for JM_F32, as jm_layer_fwd) */
+  int32_t act;           /* JM_ACT_* */
+} jm_linear_dims;
+
+/* Matrix product with bias, activation and residual in its epilogue:
+ *   p = x . w^T + bias;  out = act(p) + residual
+ *   x         in:  [rows, in_features];  w in: [out_features, in_features]
+ *   bias      in:  [out_features] or NULL
+ *   residual  in:  [rows, out_features] or NULL; may be the same buffer as out
+ *   out       out: [rows, out_features]
+ *   pre       out: [rows, out_features], p rounded to bf16, for jm_linear_bwd, or NULL
+ * The products run on tcgen05 with float32 accumulation; out and pre are rounded
+ * once.  Any other overlap of an output with an input or output is refused.
+ * Workspace: jm_linear_fwd_workspace_size(dims) bytes, 256-byte aligned; its first
+ * 256 bytes are the error header jm_poll_error reads. */
+size_t jm_linear_fwd_workspace_size(const jm_linear_dims* dims);
+jm_status jm_linear_fwd(const jm_linear_dims* dims, const void* x, const void* w, const void* bias,
+                        const void* residual, void* out, void* pre, void* workspace,
+                        size_t ws_bytes, jm_stream_t stream);
+
+/* Backward of jm_linear_fwd.  Given g_out = dLoss/dout (which is the residual's
+ * gradient too):
+ *   g_p = g_out act'(p), rounded to bf16 as the tensor cores' operand;
+ *   g_x = g_p . w,  g_w = g_p^T . x,  g_bias = sum over rows of g_out act'(p)
+ *   pre       in:  [rows, out_features] as jm_linear_fwd wrote it; NULL for JM_ACT_NONE
+ *   g_x out: [rows, in_features];  g_w out: [out_features, in_features];
+ *   g_bias out: [out_features]; each may be NULL (then it is not computed).  x is read
+ *             for g_w only and w for g_x only (either may be NULL otherwise).
+ * Sums are float32 in a fixed order: two runs give the same bits.  Overlap of an
+ * output with an input or another output is refused.  Workspace as above. */
+size_t jm_linear_bwd_workspace_size(const jm_linear_dims* dims);
+jm_status jm_linear_bwd(const jm_linear_dims* dims, const void* g_out, const void* x,
+                        const void* w, const void* pre, void* g_x, void* g_w, void* g_bias,
+                        void* workspace, size_t ws_bytes, jm_stream_t stream);
+
 /* Failure-detection self-test: launches one thread that waits, through the
  * same bounded wait the pipelines use, on a barrier that nothing completes.
  * The wait gives up after its limit (2 s), records site 99 in workspace's

@@ -1,4 +1,4 @@
-// The C ABI of the decoder block's operators around the mixer (norms): host-side
+// The C ABI of the decoder block's operators around the mixer (norms, linear): host-side
 // validation, workspace sizing and dispatch.
 #include <string.h>
 
@@ -218,4 +218,151 @@ JM_API jm_status jm_norm_bwd(const jm_norm_dims* dims, const void* g_y, const vo
   a.g_x = g_x;
   return finish_call(p, run_norm_bwd(a, g_weight, g_bias, static_cast<char*>(workspace), dims->io,
                                      p));
+}
+
+namespace jmix {
+namespace {
+
+jm_status check_linear_dims(const jm_linear_dims* d) {
+  if (!d) {
+    set_error("dims is NULL");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->io != JM_F32 && d->io != JM_BF16) {
+    set_error("io dtype must be JM_F32 or JM_BF16");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->io != JM_BF16) {
+    set_error("the linear operators are built for bf16 io only");
+    return JM_ERR_UNSUPPORTED;
+  }
+  if (d->act < JM_ACT_NONE || d->act > JM_ACT_SILU) {
+    set_error("act must be one of JM_ACT_*");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->rows < 0 || d->in_features <= 0 || d->out_features <= 0) {
+    set_error("sizes must be positive (rows >= 0)");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->in_features % 8 || d->out_features % 8) {
+    set_error("in_features and out_features must be multiples of 8 (got %lld, %lld)",
+              (long long)d->in_features, (long long)d->out_features);
+    return JM_ERR_INVALID_ARG;
+  }
+  const int64_t most = 0x7fffff00LL;  // coordinates of the tensor maps are 32-bit
+  if (d->rows > most || d->in_features > most || d->out_features > most ||
+      (double)d->rows * (double)d->in_features > 1.0e12 ||
+      (double)d->rows * (double)d->out_features > 1.0e12 ||
+      (double)d->in_features * (double)d->out_features > 1.0e12) {
+    set_error("problem too large");
+    return JM_ERR_INVALID_ARG;
+  }
+  return JM_OK;
+}
+
+// No output may overlap an input or another output.
+jm_status check_disjoint(const Arg* out, int n_out, const Arg* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(out[i], in[j])) return refuse_overlap(out[i], in[j]);
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return refuse_overlap(out[i], out[j]);
+  }
+  return JM_OK;
+}
+
+}  // namespace
+}  // namespace jmix
+
+JM_API size_t jm_linear_fwd_workspace_size(const jm_linear_dims* dims) {
+  if (check_linear_dims(dims) != JM_OK) return 0;
+  return linear_fwd_ws_bytes(dims->rows, dims->in_features, dims->out_features);
+}
+
+JM_API size_t jm_linear_bwd_workspace_size(const jm_linear_dims* dims) {
+  if (check_linear_dims(dims) != JM_OK) return 0;
+  return linear_bwd_ws_bytes(dims->rows, dims->in_features, dims->out_features, dims->act);
+}
+
+JM_API jm_status jm_linear_fwd(const jm_linear_dims* dims, const void* x, const void* w,
+                               const void* bias, const void* residual, void* out, void* pre,
+                               void* workspace, size_t ws_bytes, jm_stream_t stream) {
+  jm_status st = check_linear_dims(dims);
+  if (st != JM_OK) return st;
+  const size_t M = (size_t)dims->rows, K = (size_t)dims->in_features,
+               N = (size_t)dims->out_features;
+  const bool any = M > 0;
+  const size_t need = jm_linear_fwd_workspace_size(dims);
+  // the residual is checked apart: it may be exactly out's buffer (each value is read
+  // by the thread that then writes it)
+  const Arg in[] = {{"x", x, M * K * 2, any},
+                    {"w", w, N * K * 2, true},
+                    {"bias", bias, N * 2, false},
+                    {"residual", residual, M * N * 2, false}};
+  const Arg outs[] = {{"out", out, M * N * 2, any},
+                      {"pre", pre, M * N * 2, false},
+                      {"workspace", workspace, need, false}};
+  if ((st = check_args(in, 4)) != JM_OK || (st = check_args(outs, 2)) != JM_OK) return st;
+  if ((st = check_workspace("jm_linear_fwd", workspace, ws_bytes, need)) != JM_OK) return st;
+  if ((st = check_disjoint(outs, 3, in, residual == out ? 3 : 4)) != JM_OK) return st;
+  if (residual == out)
+    for (int i = 1; i < 3; ++i)
+      if (overlap(outs[i], in[3])) return refuse_overlap(outs[i], in[3]);
+  Problem p;
+  begin_call(p, stream);
+  LinearArgs a{};
+  a.M = dims->rows;
+  a.K = dims->in_features;
+  a.N = dims->out_features;
+  a.act = dims->act;
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.residual = residual;
+  a.out = out;
+  a.pre = pre;
+  a.ws = static_cast<char*>(workspace);
+  return finish_call(p, run_linear_fwd(a, p));
+}
+
+JM_API jm_status jm_linear_bwd(const jm_linear_dims* dims, const void* g_out, const void* x,
+                               const void* w, const void* pre, void* g_x, void* g_w, void* g_bias,
+                               void* workspace, size_t ws_bytes, jm_stream_t stream) {
+  jm_status st = check_linear_dims(dims);
+  if (st != JM_OK) return st;
+  const size_t M = (size_t)dims->rows, K = (size_t)dims->in_features,
+               N = (size_t)dims->out_features;
+  const bool any = M > 0, act = dims->act != JM_ACT_NONE;
+  if (pre && !act) {
+    set_error("pre must be NULL for JM_ACT_NONE");
+    return JM_ERR_INVALID_ARG;
+  }
+  const size_t need = jm_linear_bwd_workspace_size(dims);
+  const Arg in[] = {{"g_out", g_out, M * N * 2, any},
+                    {"x", x, M * K * 2, any && g_w},
+                    {"w", w, N * K * 2, any && g_x},
+                    {"pre", pre, M * N * 2, any && act}};
+  const Arg outs[] = {{"g_x", g_x, M * K * 2, false},
+                      {"g_w", g_w, N * K * 2, false},
+                      {"g_bias", g_bias, N * 2, false},
+                      {"workspace", workspace, need, false}};
+  if ((st = check_args(in, 4)) != JM_OK || (st = check_args(outs, 3)) != JM_OK) return st;
+  if ((st = check_workspace("jm_linear_bwd", workspace, ws_bytes, need)) != JM_OK) return st;
+  if ((st = check_disjoint(outs, 4, in, 4)) != JM_OK) return st;
+  Problem p;
+  begin_call(p, stream);
+  LinearArgs a{};
+  a.M = dims->rows;
+  a.K = dims->in_features;
+  a.N = dims->out_features;
+  a.act = dims->act;
+  a.g_out = g_out;
+  a.x = x;
+  a.w = w;
+  a.pre = const_cast<void*>(pre);
+  a.g_x = g_x;
+  a.g_w = g_w;
+  a.g_bias = g_bias;
+  a.ws = static_cast<char*>(workspace);
+  return finish_call(p, run_linear_bwd(a, p));
 }

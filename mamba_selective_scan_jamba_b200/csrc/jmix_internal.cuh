@@ -128,6 +128,27 @@ size_t norm_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t x_stride, jm_dtype 
 cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p);
 cudaError_t run_norm_bwd(NormBwdArgs a, void* g_w, void* g_b, char* ws, jm_dtype io, Problem& p);
 
+// The linear operator of k_linear.cu after validation.
+struct LinearArgs {
+  int64_t M, K, N;       // rows, in_features, out_features
+  int act;
+  const void* x;
+  const void* w;
+  const void* bias;      // forward, may be null
+  const void* residual;  // forward, may be null
+  void* out;
+  void* pre;             // forward out (may be null); backward in (null for JM_ACT_NONE)
+  const void* g_out;     // backward
+  void* g_x;             // may be null
+  void* g_w;             // may be null
+  void* g_bias;          // may be null
+  char* ws;
+};
+size_t linear_fwd_ws_bytes(int64_t M, int64_t K, int64_t N);
+size_t linear_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, int act);
+cudaError_t run_linear_fwd(const LinearArgs& a, Problem& p);
+cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p);
+
 // Launch accounting of a call outside the mixer: an empty Problem on `stream`
 // with this thread's timing events, and the status of its end.
 void begin_call(Problem& p, jm_stream_t stream);

@@ -1,0 +1,629 @@
+// Linear layers of the decoder block on tcgen05 tensor cores:
+//   forward   out = act(x w^T + bias) + residual
+//   backward  g_p = g_out act'(p);  g_x = g_p w;  g_w = g_p^T x;  g_bias = sum g_p
+//
+// All three products are C[M, N] = sum_k A[m, k] B[n, k] with bf16 operands and
+// float32 accumulation in TMEM; they differ in which index of an operand is
+// contiguous in memory:
+//   forward  A = x   [m, k] K-major,            B = w   [n, k] K-major
+//   g_x      A = g_p [m, n] K-major,            B = w   [n, k] read as B[k, n]: MN-major
+//   g_w      A = g_p [m, n] read as A[n, m]: MN-major,  B = x [m, k] read as B[k, m]: MN-major
+// tcgen05 takes either major order from a 128-byte-swizzled tile, so nothing is
+// transposed in memory.
+//
+// k_linear_pair: persistent CTA pairs (cluster of 2, cta_group::2), a 256 x BN tile
+// per pair, 64-wide K chunks in a TMA ring, the leader issues the MMAs, each CTA
+// drains its 128 rows from one of two accumulators while the next tile fills the
+// other.  Problems with few tiles are cut along K (`splits`): the work items write
+// float32 partial tiles and k_linear_reduce adds them in a fixed order and applies
+// the epilogue.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "block_math.cuh"
+#include "jmix_internal.cuh"
+#include "sm100.cuh"
+
+namespace jmix {
+namespace {
+
+using namespace sm100;
+
+constexpr int kK = 64;              // K chunk: one 128-byte swizzle atom of bf16
+constexpr int kHalf = 128;          // tile rows per CTA
+constexpr int kThreads = 192;
+constexpr int kGroupM = 16;         // row tiles per raster group
+constexpr uint32_t kTmemCols = 512;
+constexpr int kABytes = kHalf * kK * 2;                      // 16 KB
+constexpr int b_bytes(int BN) { return BN / 2 * kK * 2; }    // 16 or 8 KB
+constexpr int stage_bytes(int BN) { return kABytes + b_bytes(BN); }
+constexpr int stages(int BN) { return BN == 256 ? 6 : 8; }
+constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 256; }
+
+struct Epilogue {
+  const __nv_bfloat16* bias;      // [N] or null
+  const __nv_bfloat16* residual;  // [M, N] or null
+  __nv_bfloat16* out;             // [M, N]
+  __nv_bfloat16* pre;             // [M, N] or null
+  int act;
+};
+
+struct PairArgs {
+  int64_t M, N, K;
+  int64_t m_tiles, n_tiles;
+  int splits;
+  float* part;   // [splits][M][N] when splits > 1
+  Epilogue ep;
+  ErrFlags* err;
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// Bias, activation and residual on 8 consecutive columns of one row, and the stores.
+__device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_t at, int64_t col) {
+  if (e.bias) {
+    float b[8];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(e.bias + col)), b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += b[j];
+  }
+  if (e.pre) *reinterpret_cast<uint4*>(e.pre + at) = pack8(v);
+  if (e.act != JM_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = act_apply(v[j], e.act);
+  }
+  if (e.residual) {
+    float r[8];
+    unpack8(*reinterpret_cast<const uint4*>(e.residual + at), r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += r[j];
+  }
+  *reinterpret_cast<uint4*>(e.out + at) = pack8(v);
+}
+
+struct Item {
+  int64_t mt, nt;
+  int k0, k1;    // K chunks [k0, k1)
+  int split;
+};
+
+__device__ __forceinline__ Item item_of(const PairArgs& g, int64_t w, int kchunks) {
+  Item it;
+  const int64_t tiles = g.m_tiles * g.n_tiles;
+  it.split = (int)(w / tiles);
+  const int64_t t = w - (int64_t)it.split * tiles;
+  const int64_t per_group = (int64_t)kGroupM * g.n_tiles;
+  const int64_t grp = t / per_group, idx = t - grp * per_group;
+  const int64_t rows = min((int64_t)kGroupM, g.m_tiles - grp * kGroupM);
+  it.mt = grp * kGroupM + idx % rows;
+  it.nt = idx / rows;
+  it.k0 = (int)((int64_t)kchunks * it.split / g.splits);
+  it.k1 = (int)((int64_t)kchunks * (it.split + 1) / g.splits);
+  return it;
+}
+
+template <bool AMN, bool BMN, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                  const PairArgs g) {
+  constexpr int S = stages(BN), kStage = stage_bytes(BN), kBHalf = BN / 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kStage);
+  uint64_t* full = bars;              // [S] (leader) both CTAs' halves landed
+  uint64_t* empty = bars + S;         // [S] the pair's MMAs have read the stage
+  uint64_t* acc_full = bars + 2 * S;  // [2] accumulator complete
+  uint64_t* acc_empty = acc_full + 2; // [2] (leader) both epilogues are done (8 warps)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int64_t items = g.m_tiles * g.n_tiles * g.splits;
+  const int kchunks = (int)((g.K + kK - 1) / kK);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), 8);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_a);
+    prefetch_tmap(&tm_b);
+  }
+  tc_fence_before();
+  cluster_sync();   // both CTAs' barriers exist before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int64_t it = 0;
+      bool ok = true;
+      for (int64_t w = pair; ok && w < items; w += npairs) {
+        const Item q = item_of(g, w, kchunks);
+        const int32_t m0 = (int32_t)(q.mt * (2 * kHalf) + rank * kHalf);
+        const int32_t n0 = (int32_t)(q.nt * BN + rank * kBHalf);
+        for (int kc = q.k0; kc < q.k1; ++kc, ++it) {
+          const int s = (int)(it % S);
+          if (it >= S &&
+              !mbar_wait(smem_u32(&empty[s]), (uint32_t)((it / S) - 1) & 1u, g.err, 81)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = smem_u32(smem + s * kStage);
+          const uint32_t fb = leader_addr(smem_u32(&full[s]));
+          // the leader expects both CTAs' bytes on its barrier
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), (uint32_t)(2 * kStage));
+          if constexpr (AMN) {   // boxes of 64 m values x 64 k rows
+            tma_load_2d_pair(st, &tm_a, fb, m0, kc * kK);
+            tma_load_2d_pair(st + kABytes / 2, &tm_a, fb, m0 + 64, kc * kK);
+          } else {
+            tma_load_2d_pair(st, &tm_a, fb, kc * kK, m0);
+          }
+          if constexpr (BMN) {
+#pragma unroll
+            for (int h = 0; h < kBHalf / 64; ++h)
+              tma_load_2d_pair(st + kABytes + h * 8192, &tm_b, fb, n0 + 64 * h, kc * kK);
+          } else {
+            tma_load_2d_pair(st + kABytes, &tm_b, fb, kc * kK, n0);
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      const uint32_t idesc = idesc_bf16_f32_major(2 * kHalf, BN, AMN, BMN);
+      int64_t it = 0, j = 0;
+      bool ok = true;
+      for (int64_t w = pair; ok && w < items; w += npairs, ++j) {
+        const Item q = item_of(g, w, kchunks);
+        const int b = (int)(j & 1);
+        if (j >= 2 && !mbar_wait(smem_u32(&acc_empty[b]), (uint32_t)((j >> 1) - 1) & 1u, g.err, 82))
+          break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + (uint32_t)(b * 256);
+        for (int kc = q.k0; kc < q.k1; ++kc, ++it) {
+          const int s = (int)(it % S);
+          if (!mbar_wait(smem_u32(&full[s]), (uint32_t)(it / S) & 1u, g.err, 83)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ab = smem_u32(smem + s * kStage), bb = ab + kABytes;
+#pragma unroll
+          for (int kk = 0; kk < kK / 16; ++kk) {
+            const uint64_t ad = AMN ? sw128_mnmajor_desc(ab + kk * 2048, 8192)
+                                    : sw128_kmajor_desc(ab + kk * 32);
+            const uint64_t bd = BMN ? sw128_mnmajor_desc(bb + kk * 2048, 8192)
+                                    : sw128_kmajor_desc(bb + kk * 32);
+            umma_f16_pair(d_tmem, ad, bd, idesc, (kc > q.k0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit_pair(smem_u32(&empty[s]), 0x3);
+        }
+        if (ok) umma_commit_pair(smem_u32(&acc_full[b]), 0x3);
+      }
+    }
+  } else {
+    // epilogue: this CTA's 128 rows of the pair's 256-row tile, a row per thread
+    const int lg = warp & 3;
+    const uint32_t acc_empty_leader = leader_addr(smem_u32(&acc_empty[0]));
+    int64_t j = 0;
+    for (int64_t w = pair; w < items; w += npairs, ++j) {
+      const Item q = item_of(g, w, kchunks);
+      const int b = (int)(j & 1);
+      if (!mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(j >> 1) & 1u, g.err, 84)) break;
+      tc_fence_after();
+      const int64_t row = q.mt * (2 * kHalf) + rank * kHalf + lg * 32 + lane;
+      const int64_t n0 = q.nt * BN;
+      const uint32_t tbase = tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(b * 256);
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        if (n0 + c >= g.N) break;
+        uint32_t r[32];
+        tmem_ld16(tbase + (uint32_t)c, *reinterpret_cast<uint32_t(*)[16]>(r));
+        tmem_ld16(tbase + (uint32_t)(c + 16), *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+        tmem_ld_wait();
+        if (row < g.M) {
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {  // 8 columns at a time
+            const int64_t col = n0 + c + 8 * o;
+            if (col + 8 > g.N) break;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * o + i]);
+            const int64_t at = row * g.N + col;
+            if (g.splits > 1) {
+              float4* dst = reinterpret_cast<float4*>(g.part + (int64_t)q.split * g.M * g.N + at);
+              dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+              dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+              finish8(g.ep, v, at, col);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_empty_leader + (uint32_t)(b * 8));
+    }
+  }
+  tc_fence_before();
+  cluster_sync();   // no CTA leaves while its pair may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// The partial tiles of a K split, added in split order, then the epilogue.
+__global__ void __launch_bounds__(256)
+    k_linear_reduce(const float* __restrict__ part, int splits, int64_t M, int64_t N,
+                    const Epilogue ep) {
+  grid_dep_wait();
+  const int64_t n8 = N / 8, total = M * n8;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / n8, col = (i - row * n8) * 8, at = row * N + col;
+    float v[8] = {};
+    for (int s = 0; s < splits; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(part + (int64_t)s * M * N + at);
+      const float4 a = __ldcs(p), b = __ldcs(p + 1);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    finish8(ep, v, at, col);
+  }
+}
+
+// g_p = g_out act'(pre) in bf16 (the operand of both products) and, for g_bias, its
+// column sums (unrounded, float32) over this CTA's rows.  A CTA takes 2048 columns
+// (8 per thread) x `rows` rows; one read of g_out and pre, one write of g_p.
+constexpr int kGpCols = 2048;
+
+__global__ void __launch_bounds__(256)
+    k_linear_gpre(const __nv_bfloat16* __restrict__ g_out, const __nv_bfloat16* __restrict__ pre,
+                  int act, int64_t M, int64_t N, int rows, __nv_bfloat16* __restrict__ gp,
+                  float* __restrict__ part, ErrFlags* err) {
+  grid_dep_wait();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(ErrFlags) / 4)
+    reinterpret_cast<unsigned*>(err)[threadIdx.x] = 0u;
+  const int64_t col = (int64_t)blockIdx.x * kGpCols + threadIdx.x * 8;
+  if (col >= N) return;
+  const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = min(M, r0 + rows);
+  float sum[8] = {};
+#pragma unroll 4
+  for (int64_t r = r0; r < r1; ++r) {
+    float g[8];
+    unpack8(*reinterpret_cast<const uint4*>(g_out + r * N + col), g);
+    if (pre) {
+      float p[8];
+      unpack8(*reinterpret_cast<const uint4*>(pre + r * N + col), p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] *= act_grad(p[j], act);
+      *reinterpret_cast<uint4*>(gp + r * N + col) = pack8(g);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += g[j];
+  }
+  if (part) {
+    float4* d = reinterpret_cast<float4*>(part + (int64_t)blockIdx.y * N + col);
+    d[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    d[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+  }
+}
+
+// Column sums of the partial rows in a fixed order (16 interleaved chains).
+__global__ void __launch_bounds__(512)
+    k_linear_bias_reduce(const float* __restrict__ part, int64_t rows, int64_t N,
+                         __nv_bfloat16* __restrict__ g_bias) {
+  __shared__ float sh[16][33];
+  grid_dep_wait();
+  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  float acc = 0.0f;
+  if (c < N)
+    for (int64_t r = threadIdx.y; r < rows; r += 16) acc += part[r * N + c];
+  sh[threadIdx.y][threadIdx.x] = acc;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < N) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) acc += sh[i][threadIdx.x];
+    g_bias[c] = __float2bfloat16_rn(acc);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::atomic<EncodeTiledFn> fn{nullptr};
+  EncodeTiledFn f = fn.load(std::memory_order_relaxed);
+  if (!f) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      f = reinterpret_cast<EncodeTiledFn>(p);
+    fn.store(f, std::memory_order_relaxed);
+  }
+  return f;
+}
+
+// A row-major bf16 matrix [outer][inner] as boxes of 64 inner values x `box` rows.
+bool bf16_map(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, int box) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
+  cuuint32_t bx[2] = {(cuuint32_t)kK, (cuuint32_t)box}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kPairs = 74;   // CTA pairs of a B200 (148 SMs)
+
+// How a product is cut: tile width and K splits.
+struct Cut {
+  int bn, splits;
+};
+
+// Estimated microseconds: waves of work items on 74 pairs (a 64-wide chunk of a 256 x
+// 256 tile takes a pair 0.4 us, of a 256 x 128 tile 0.23), ~2 us for the first fill and
+// last drain, and for splits the partial tiles' round trip through L2 and one launch.
+Cut choose_cut(int64_t M, int64_t N, int64_t K) {
+  const int64_t chunks = (K + kK - 1) / kK;
+  Cut best{256, 1};
+  double best_us = 1e30;
+  for (int bn = 256; bn >= 128; bn /= 2) {
+    const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn);
+    const double chunk_us = bn == 256 ? 0.40 : 0.23;
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && chunks / s < 4) break;
+      const int64_t waves = (tiles * s + kPairs - 1) / kPairs;
+      double us = (double)waves * (double)((chunks + s - 1) / s) * chunk_us + 2.0;
+      if (s > 1) us += 3.0 + (double)M * (double)N * 4.0 * (2 * s + 1) / 6.0e6;
+      if (us < best_us * 0.999) {
+        best_us = us;
+        best = {bn, s};
+      }
+    }
+  }
+  return best;
+}
+
+size_t part_bytes(int64_t M, int64_t N, int64_t K) {
+  const Cut c = choose_cut(M, N, K);
+  return c.splits > 1 ? align256((size_t)c.splits * M * N * 4) : 0;
+}
+
+int cached_attr(std::atomic<int>* cache, int dev, int (*query)()) {
+  if (dev < 0 || dev >= 64) return query();
+  int v = cache[dev].load(std::memory_order_relaxed);
+  if (!v) cache[dev].store(v = query(), std::memory_order_relaxed);
+  return v;
+}
+
+template <bool AMN, bool BMN, int BN>
+int query_pairs() {
+  auto kern = k_linear_pair<AMN, BMN, BN>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN)) !=
+      cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * kPairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes(BN);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  return n;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                   Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <bool AMN, bool BMN, int BN>
+cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& g,
+                        cudaStream_t s) {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int most = cached_attr(cache, dev, query_pairs<AMN, BMN, BN>);
+  if (most <= 0) return cudaErrorInvalidConfiguration;
+  const int64_t items = g.m_tiles * g.n_tiles * g.splits;
+  const int64_t pairs = items < most ? items : most;
+  return launch(k_linear_pair<AMN, BMN, BN>, dim3((unsigned)(2 * pairs)), dim3(kThreads),
+                (size_t)smem_bytes(BN), s, ta, tb, g);
+}
+
+// C[M, N] = A . B^T with the epilogue `ep`.  AMN / BMN: A is stored [K, M], B [K, N].
+template <bool AMN, bool BMN>
+cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* B,
+                    const Epilogue& ep, float* part, ErrFlags* err, Problem& p) {
+  const Cut c = choose_cut(M, N, K);
+  CUtensorMap ta, tb;
+  const bool ok = (AMN ? bf16_map(&ta, A, K, M, 64) : bf16_map(&ta, A, M, K, kHalf)) &&
+                  (BMN ? bf16_map(&tb, B, K, N, 64) : bf16_map(&tb, B, N, K, c.bn / 2));
+  if (!ok) return cudaErrorInvalidValue;
+  PairArgs g{};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.m_tiles = (M + 255) / 256;
+  g.n_tiles = (N + c.bn - 1) / c.bn;
+  g.splits = c.splits;
+  g.part = part;
+  g.ep = ep;
+  g.err = err;
+  cudaError_t e = c.bn == 256 ? launch_pair<AMN, BMN, 256>(ta, tb, g, p.stream)
+                              : launch_pair<AMN, BMN, 128>(ta, tb, g, p.stream);
+  if (e != cudaSuccess) return e;
+  launched(p, "k_linear_pair");
+  if (c.splits > 1) {
+    const int64_t n = M * N / 8;
+    const int64_t ctas = (n + 255) / 256 < 148 * 8 ? (n + 255) / 256 : 148 * 8;
+    e = launch(k_linear_reduce, dim3((unsigned)ctas), dim3(256), 0, p.stream, (const float*)part,
+               c.splits, M, N, ep);
+    if (e == cudaSuccess) launched(p, "k_linear_reduce");
+  }
+  return e;
+}
+
+// Rows a CTA of k_linear_gpre takes: enough CTAs for the GPU, at most 64 rows each.
+int gpre_rows(int64_t M, int64_t N) {
+  const int64_t col_ctas = (N + kGpCols - 1) / kGpCols;
+  int64_t r = (M * col_ctas + 148 * 8 - 1) / (148 * 8);
+  r = r < 4 ? 4 : r;
+  if (r < (M + 65534) / 65535) r = (M + 65534) / 65535;   // grid y limit
+  return (int)r;
+}
+
+// Backward workspace: [header][g_p bf16][bias partial rows][partial tiles of the
+// larger split product].
+struct BwdWs {
+  __nv_bfloat16* gp;
+  float* bias_part;
+  float* part;
+  size_t bytes;
+};
+
+BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int act, char* base) {
+  BwdWs w{};
+  size_t off = sizeof(ErrFlags);
+  auto take = [&](size_t n) {
+    char* p = base ? base + off : nullptr;
+    off += align256(n);
+    return p;
+  };
+  w.gp = reinterpret_cast<__nv_bfloat16*>(take(act == JM_ACT_NONE ? 0 : (size_t)M * N * 2));
+  const int64_t rows = M ? (M + gpre_rows(M, N) - 1) / gpre_rows(M, N) : 0;
+  w.bias_part = reinterpret_cast<float*>(take((size_t)rows * N * 4));
+  const size_t px = M ? part_bytes(M, K, N) : 0, pw = M ? part_bytes(N, K, M) : 0;
+  w.part = reinterpret_cast<float*>(take(px > pw ? px : pw));
+  w.bytes = off;
+  return w;
+}
+
+}  // namespace
+
+size_t linear_fwd_ws_bytes(int64_t M, int64_t K, int64_t N) {
+  return sizeof(ErrFlags) + (M ? part_bytes(M, N, K) : 0);
+}
+
+size_t linear_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
+  return bwd_ws(M, K, N, act, nullptr).bytes;
+}
+
+cudaError_t run_linear_fwd(const LinearArgs& a, Problem& p) {
+  ErrFlags* err = reinterpret_cast<ErrFlags*>(a.ws);
+  cudaError_t e = cudaMemsetAsync(err, 0, sizeof(ErrFlags), p.stream);
+  if (e != cudaSuccess || a.M == 0) return e;
+  Epilogue ep{};
+  ep.bias = static_cast<const __nv_bfloat16*>(a.bias);
+  ep.residual = static_cast<const __nv_bfloat16*>(a.residual);
+  ep.out = static_cast<__nv_bfloat16*>(a.out);
+  ep.pre = static_cast<__nv_bfloat16*>(a.pre);
+  ep.act = a.act;
+  launches_begin(p);
+  return product<false, false>(a.M, a.N, a.K, a.x, a.w, ep,
+                               reinterpret_cast<float*>(a.ws + sizeof(ErrFlags)), err, p);
+}
+
+cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
+  ErrFlags* err = reinterpret_cast<ErrFlags*>(a.ws);
+  if (a.M == 0) {  // nothing flows back: the sums over rows are zero
+    cudaError_t e = cudaMemsetAsync(err, 0, sizeof(ErrFlags), p.stream);
+    if (e == cudaSuccess && a.g_w) e = cudaMemsetAsync(a.g_w, 0, (size_t)a.N * a.K * 2, p.stream);
+    if (e == cudaSuccess && a.g_bias) e = cudaMemsetAsync(a.g_bias, 0, (size_t)a.N * 2, p.stream);
+    return e;
+  }
+  const BwdWs w = bwd_ws(a.M, a.K, a.N, a.act, a.ws);
+  const void* gp = a.g_out;
+  cudaError_t e = cudaSuccess;
+  launches_begin(p);
+  const bool grad = a.act != JM_ACT_NONE && (a.g_x || a.g_w || a.g_bias);
+  if (grad || a.g_bias) {
+    const int rows = gpre_rows(a.M, a.N);
+    const dim3 grid((unsigned)((a.N + kGpCols - 1) / kGpCols), (unsigned)((a.M + rows - 1) / rows));
+    e = launch(k_linear_gpre, grid, dim3(256), 0, p.stream,
+               static_cast<const __nv_bfloat16*>(a.g_out),
+               grad ? static_cast<const __nv_bfloat16*>(a.pre) : nullptr, a.act, a.M, a.N, rows,
+               w.gp, a.g_bias ? w.bias_part : nullptr, err);
+    if (e != cudaSuccess) return e;
+    launched(p, "k_linear_gpre");
+    if (grad) gp = w.gp;
+    if (a.g_bias) {
+      e = launch(k_linear_bias_reduce, dim3((unsigned)((a.N + 31) / 32)), dim3(32, 16), 0, p.stream,
+                 (const float*)w.bias_part, (int64_t)grid.y, a.N,
+                 static_cast<__nv_bfloat16*>(a.g_bias));
+      if (e != cudaSuccess) return e;
+      launched(p, "k_linear_bias_reduce");
+    }
+  } else {
+    e = cudaMemsetAsync(err, 0, sizeof(ErrFlags), p.stream);
+    if (e != cudaSuccess) return e;
+  }
+  Epilogue ep{};
+  ep.act = JM_ACT_NONE;
+  if (a.g_x) {  // [M, K] = g_p [M, N] . w [N, K]
+    ep.out = static_cast<__nv_bfloat16*>(a.g_x);
+    e = product<false, true>(a.M, a.K, a.N, gp, a.w, ep, w.part, err, p);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.g_w) {  // [N, K] = g_p [M, N]^T . x [M, K]
+    ep.out = static_cast<__nv_bfloat16*>(a.g_w);
+    e = product<true, true>(a.N, a.K, a.M, gp, a.x, ep, w.part, err, p);
+  }
+  return e;
+}
+
+}  // namespace jmix

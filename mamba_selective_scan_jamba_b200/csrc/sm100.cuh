@@ -436,6 +436,25 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16
 }
 
+// Shared-memory matrix descriptor of an MN-major operand (its M or N index
+// contiguous) in the 128-byte-swizzled canonical layout: boxes of 64 bf16 (128 B) x
+// `k rows`, 8 k rows 1024 B apart, the next 64 M / N values `mn_stride` bytes on.  The
+// start address advances by 2048 B per K=16 step.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(mn_stride >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// idesc_bf16_f32 with MN-major A and / or B.
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_major(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_bf16_f32(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+
 // ---------------------------------------------------------------- fast math
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;

@@ -30,7 +30,9 @@ EXPORTED = ("jm_mixer_fwd_workspace_size", "jm_mixer_step_workspace_size", "jm_m
             "jm_layer_fwd_workspace_size", "jm_layer_fwd", "jm_scan_bwd_workspace_size",
             "jm_scan_bwd", "jm_scan_bwd_schedule", "jm_noalloc_poll_error",
             "jm_noalloc_selftest_timeout", "jm_prepared_weights_size", "jm_prepare_weights",
-            "jm_mixer_step_indexed", "jm_norm_fwd", "jm_norm_bwd_workspace_size", "jm_norm_bwd")
+            "jm_mixer_step_indexed", "jm_norm_fwd", "jm_norm_bwd_workspace_size", "jm_norm_bwd",
+            "jm_linear_fwd_workspace_size", "jm_linear_fwd", "jm_linear_bwd_workspace_size",
+            "jm_linear_bwd")
 
 
 class jm_dims(ctypes.Structure):
@@ -45,6 +47,11 @@ class jm_norm_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("x_stride", ctypes.c_int64),
                 ("eps", ctypes.c_float), ("io", ctypes.c_int), ("kind", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class jm_linear_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_features", ctypes.c_int64),
+                ("out_features", ctypes.c_int64), ("io", ctypes.c_int), ("act", ctypes.c_int32)]
 
 
 class JmixError(RuntimeError):
@@ -116,6 +123,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.jm_norm_bwd.restype = ctypes.c_int
     lib.jm_norm_bwd.argtypes = ([ctypes.POINTER(jm_norm_dims)] + [_vp] * 9
                                 + [ctypes.c_size_t, _vp])
+    for f in (lib.jm_linear_fwd_workspace_size, lib.jm_linear_bwd_workspace_size):
+        f.restype = ctypes.c_size_t
+        f.argtypes = [ctypes.POINTER(jm_linear_dims)]
+    lib.jm_linear_fwd.restype = ctypes.c_int
+    lib.jm_linear_fwd.argtypes = ([ctypes.POINTER(jm_linear_dims)] + [_vp] * 7
+                                  + [ctypes.c_size_t, _vp])
+    lib.jm_linear_bwd.restype = ctypes.c_int
+    lib.jm_linear_bwd.argtypes = ([ctypes.POINTER(jm_linear_dims)] + [_vp] * 8
+                                  + [ctypes.c_size_t, _vp])
     lib.jm_noalloc_poll_error.restype = ctypes.c_int
     lib.jm_noalloc_poll_error.argtypes = [_vp]
     lib.jm_noalloc_selftest_timeout.restype = ctypes.c_int
@@ -148,6 +164,14 @@ JM_NORM_RMS, JM_NORM_LAYER = 0, 1
 def norm_dims(rows: int, cols: int, io: int = JM_BF16, kind: int = JM_NORM_RMS,
               eps: float = 1e-6, x_stride: Optional[int] = None) -> jm_norm_dims:
     return jm_norm_dims(rows, cols, cols if x_stride is None else x_stride, eps, io, kind, 0)
+
+
+JM_ACT_NONE, JM_ACT_RELU, JM_ACT_GELU, JM_ACT_SILU = range(4)
+
+
+def linear_dims(rows: int, in_features: int, out_features: int, act: int = JM_ACT_NONE,
+                io: int = JM_BF16) -> jm_linear_dims:
+    return jm_linear_dims(rows, in_features, out_features, io, act)
 
 
 def _ptr(t) -> Optional[int]:
@@ -295,6 +319,34 @@ def jm_norm_bwd(d: jm_norm_dims, g_y, x, weight, stats, g_x, workspace, ws_bytes
     p = _tensors(d.io, g_y=g_y, x_rows=x, weight=weight, stats_f32=stats, g_sum=g_sum, g_x=g_x,
                  g_weight=g_weight, g_bias=g_bias)
     st = load().jm_norm_bwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def jm_linear_fwd_workspace_size(d: jm_linear_dims) -> int:
+    return load().jm_linear_fwd_workspace_size(ctypes.byref(d))
+
+
+def jm_linear_fwd(d: jm_linear_dims, x, w, out, workspace, ws_bytes: int, bias=None, residual=None,
+                  pre=None, stream=None, check: bool = True) -> int:
+    """out = act(x . w^T + bias) + residual (see include/jmix.h)."""
+    p = _tensors(d.io, x=x, w=w, bias=bias, residual=residual, out=out, pre=pre)
+    st = load().jm_linear_fwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def jm_linear_bwd_workspace_size(d: jm_linear_dims) -> int:
+    return load().jm_linear_bwd_workspace_size(ctypes.byref(d))
+
+
+def jm_linear_bwd(d: jm_linear_dims, g_out, x, w, workspace, ws_bytes: int, pre=None, g_x=None,
+                  g_w=None, g_bias=None, stream=None, check: bool = True) -> int:
+    """Backward of jm_linear_fwd (see include/jmix.h)."""
+    p = _tensors(d.io, g_out=g_out, x=x, w=w, pre=pre, g_x=g_x, g_w=g_w, g_bias=g_bias)
+    st = load().jm_linear_bwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
     if check:
         _check(st)
     return st

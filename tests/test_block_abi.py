@@ -108,3 +108,65 @@ def test_binding_checks_tensors():
         jmix.jm_norm_fwd(jmix.norm_dims(4, 32), F, F, F, stats=t, stream=0)
     with pytest.raises(jmix.JmixError, match="CUDA device"):
         jmix.jm_norm_fwd(jmix.norm_dims(4, 32), t, F, F, stream=0)
+
+
+def linear_fwd(d, nbytes=None, **over):
+    a = dict(x=F, w=F + G, out=F + 2 * G, workspace=W,
+             ws_bytes=jmix.jm_linear_fwd_workspace_size(d) if nbytes is None else nbytes)
+    a.update(over)
+    return jmix.jm_linear_fwd(d, **a, stream=0, check=False)
+
+
+def linear_bwd(d, nbytes=None, **over):
+    a = dict(g_out=F, x=F + G, w=F + 2 * G, g_x=F + 3 * G, g_w=F + 4 * G, g_bias=F + 5 * G,
+             workspace=W,
+             ws_bytes=jmix.jm_linear_bwd_workspace_size(d) if nbytes is None else nbytes)
+    a.update(over)
+    return jmix.jm_linear_bwd(d, **a, stream=0, check=False)
+
+
+@pytest.mark.parametrize("over,code,msg", [
+    (dict(rows=-1), jmix.JM_ERR_INVALID_ARG, "positive"),
+    (dict(in_features=0), jmix.JM_ERR_INVALID_ARG, "positive"),
+    (dict(in_features=60), jmix.JM_ERR_INVALID_ARG, "multiples of 8"),
+    (dict(out_features=12), jmix.JM_ERR_INVALID_ARG, "multiples of 8"),
+    (dict(io=jmix.JM_F32), jmix.JM_ERR_UNSUPPORTED, "bf16"),
+    (dict(io=9), jmix.JM_ERR_INVALID_ARG, "io dtype"),
+    (dict(act=4), jmix.JM_ERR_INVALID_ARG, "act"),
+    (dict(rows=1 << 31), jmix.JM_ERR_INVALID_ARG, "large"),
+])
+def test_linear_rejects_bad_dims(over, code, msg):
+    kw = dict(rows=4, in_features=64, out_features=128)
+    kw.update(over)
+    d = jmix.linear_dims(**kw)
+    assert linear_fwd(d, 1 << 30) == code and msg in jmix.jm_last_error()
+    assert linear_bwd(d, 1 << 30) == code and msg in jmix.jm_last_error()
+    assert jmix.jm_linear_fwd_workspace_size(d) == 0
+    assert jmix.jm_linear_bwd_workspace_size(d) == 0
+
+
+def test_linear_rejects_bad_pointers():
+    bad = jmix.JM_ERR_INVALID_ARG
+    d = jmix.linear_dims(4, 64, 128, act=jmix.JM_ACT_SILU)
+    for k in ("x", "w", "out"):
+        assert linear_fwd(d, **{k: None}) == bad and "NULL" in jmix.jm_last_error(), k
+        assert linear_fwd(d, **{k: F + 4}) == bad and "aligned" in jmix.jm_last_error(), k
+    assert linear_fwd(d, out=F) == bad and "out overlaps x" in jmix.jm_last_error()
+    assert linear_fwd(d, residual=F + 2 * G + 64) == bad
+    assert "out overlaps residual" in jmix.jm_last_error()
+    assert linear_fwd(d, pre=F + 2 * G) == bad and "pre overlaps out" in jmix.jm_last_error()
+    r = F + 2 * G    # residual == out, but pre over it is not
+    assert linear_fwd(d, residual=r, pre=r) == bad
+    assert linear_fwd(d, workspace=F + G) == bad and "workspace overlaps w" in jmix.jm_last_error()
+    n = jmix.jm_linear_fwd_workspace_size(d)
+    assert linear_fwd(d, nbytes=n - 1) == jmix.JM_ERR_WORKSPACE
+    assert linear_fwd(d, workspace=None) == jmix.JM_ERR_WORKSPACE
+    assert linear_fwd(d, workspace=W + 64) == jmix.JM_ERR_WORKSPACE
+    p = F + 6 * G
+    assert linear_bwd(d) == bad and "pre is NULL" in jmix.jm_last_error()
+    assert linear_bwd(jmix.linear_dims(4, 64, 128), pre=p) == bad
+    for k in ("g_out", "x", "w"):
+        assert linear_bwd(d, pre=p, **{k: None}) == bad and "NULL" in jmix.jm_last_error(), k
+    assert linear_bwd(d, pre=p, g_x=F + G) == bad and "g_x overlaps x" in jmix.jm_last_error()
+    assert linear_bwd(d, pre=p, g_w=F + 3 * G) == bad
+    assert linear_bwd(d, pre=p, nbytes=255) == jmix.JM_ERR_WORKSPACE
