@@ -396,6 +396,42 @@ jm_status jm_linear_bwd(const jm_linear_dims* dims, const void* g_out, const voi
                         const void* w, const void* pre, void* g_x, void* g_w, void* g_bias,
                         void* workspace, size_t ws_bytes, jm_stream_t stream);
 
+/* Weights of the chosen experts: JM_ROUTE_SOFTMAX_ALL takes their share of the softmax
+ * over all experts (they sum to less than 1), JM_ROUTE_SOFTMAX_TOPK the softmax over
+ * the chosen logits (they sum to 1). */
+enum { JM_ROUTE_SOFTMAX_ALL = 0, JM_ROUTE_SOFTMAX_TOPK = 1 };
+
+typedef struct {
+  int64_t tokens;     /* 0..256 (JM_ERR_UNSUPPORTED above: this is the few-token form) */
+  int64_t d_model;    /* D, positive multiple of 8 */
+  int64_t d_ff;       /* F, positive multiple of 8 */
+  int64_t n_experts;  /* E, 1..256 */
+  int64_t top_k;      /* K, 1..min(8, n_experts) */
+  jm_dtype io;        /* JM_BF16 (JM_ERR_UNSUPPORTED for JM_F32, as jm_layer_fwd) */
+  int32_t router;     /* JM_ROUTE_* */
+} jm_moe_dims;
+
+/* A whole mixture-of-experts layer for few tokens (a decode step):
+ *   logits = x . router_w^T;  e_1..e_K = the experts of the K largest logits of a token,
+ *   in falling order (a tie goes to the lower index; NaN counts as largest);
+ *   h_i = silu(x . w_gate[e_i]^T) * (x . w_up[e_i]^T), rounded to bf16;
+ *   out = sum_i weight_i h_i . w_down[e_i]^T + residual
+ *   x         in:  [tokens, D];  residual in: [tokens, D] or NULL, may be out's buffer
+ *   router_w  in:  [E, D];  w_gate, w_up in: [E, F, D];  w_down in: [E, D, F]
+ *   out       out: [tokens, D]
+ *   topk_idx  out: int32 [tokens, K], e_i, or NULL;  topk_w out: float32 [tokens, K] or NULL
+ * Logits are summed in float64, products in float32; out is rounded once.  Sums have a
+ * fixed order: two runs give the same bits.  Only the chosen experts' weights are read.
+ * Any other overlap of an output with an input or another output is refused.  Workspace:
+ * jm_moe_fwd_workspace_size(dims) bytes, 256-byte aligned; its first 256 bytes are the
+ * error header jm_poll_error reads.  The second kernel is launched cooperatively, one
+ * block on each SM of the device. */
+size_t jm_moe_fwd_workspace_size(const jm_moe_dims* dims);
+jm_status jm_moe_fwd(const jm_moe_dims* dims, const void* x, const void* router_w,
+                     const void* w_gate, const void* w_up, const void* w_down,
+                     const void* residual, void* out, int32_t* topk_idx, float* topk_w,
+                     void* workspace, size_t ws_bytes, jm_stream_t stream);
+
 /* Failure-detection self-test: launches one thread that waits, through the
  * same bounded wait the pipelines use, on a barrier that nothing completes.
  * The wait gives up after its limit (2 s), records site 99 in workspace's

@@ -1,5 +1,5 @@
-// The C ABI of the decoder block's operators around the mixer (norms, linear): host-side
-// validation, workspace sizing and dispatch.
+// The C ABI of the decoder block's operators around the mixer (norms, linear, mixture of
+// experts): host-side validation, workspace sizing and dispatch.
 #include <string.h>
 
 #include "jmix_internal.cuh"
@@ -365,4 +365,107 @@ JM_API jm_status jm_linear_bwd(const jm_linear_dims* dims, const void* g_out, co
   a.g_bias = g_bias;
   a.ws = static_cast<char*>(workspace);
   return finish_call(p, run_linear_bwd(a, p));
+}
+
+namespace jmix {
+namespace {
+
+jm_status check_moe_dims(const jm_moe_dims* d, MoeArgs* m) {
+  if (!d) {
+    set_error("dims is NULL");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->io != JM_F32 && d->io != JM_BF16) {
+    set_error("io dtype must be JM_F32 or JM_BF16");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->io != JM_BF16) {
+    set_error("the mixture-of-experts layer is built for bf16 io only");
+    return JM_ERR_UNSUPPORTED;
+  }
+  if (d->router != JM_ROUTE_SOFTMAX_ALL && d->router != JM_ROUTE_SOFTMAX_TOPK) {
+    set_error("router must be one of JM_ROUTE_*");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->tokens < 0 || d->d_model <= 0 || d->d_ff <= 0 || d->n_experts <= 0 || d->top_k <= 0) {
+    set_error("sizes must be positive (tokens >= 0)");
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->d_model % 8 || d->d_ff % 8) {
+    set_error("d_model and d_ff must be multiples of 8 (got %lld, %lld)", (long long)d->d_model,
+              (long long)d->d_ff);
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->top_k > d->n_experts) {
+    set_error("top_k %lld is more than n_experts %lld", (long long)d->top_k,
+              (long long)d->n_experts);
+    return JM_ERR_INVALID_ARG;
+  }
+  if (d->tokens > 256 || d->n_experts > 256 || d->top_k > 8) {
+    set_error("more than 256 tokens, 256 experts or top_k 8 is not built (got %lld, %lld, %lld)",
+              (long long)d->tokens, (long long)d->n_experts, (long long)d->top_k);
+    return JM_ERR_UNSUPPORTED;
+  }
+  const int64_t most = 1LL << 24;
+  m->T = d->tokens;
+  m->D = d->d_model;
+  m->F = d->d_ff;
+  m->E = d->n_experts;
+  m->topk = d->top_k;
+  m->topk_softmax = d->router == JM_ROUTE_SOFTMAX_TOPK;
+  if (m->D > most || m->F > most || !moe_fits(*m)) {
+    set_error("problem too large");
+    return JM_ERR_INVALID_ARG;
+  }
+  return JM_OK;
+}
+
+}  // namespace
+}  // namespace jmix
+
+JM_API size_t jm_moe_fwd_workspace_size(const jm_moe_dims* dims) {
+  MoeArgs m{};
+  if (check_moe_dims(dims, &m) != JM_OK) return 0;
+  return moe_ws_bytes(m);
+}
+
+JM_API jm_status jm_moe_fwd(const jm_moe_dims* dims, const void* x, const void* router_w,
+                            const void* w_gate, const void* w_up, const void* w_down,
+                            const void* residual, void* out, int32_t* topk_idx, float* topk_w,
+                            void* workspace, size_t ws_bytes, jm_stream_t stream) {
+  MoeArgs m{};
+  jm_status st = check_moe_dims(dims, &m);
+  if (st != JM_OK) return st;
+  const size_t td = (size_t)m.T * m.D * 2, w = (size_t)m.E * m.F * m.D * 2,
+               pairs = (size_t)m.T * m.topk * 4;
+  const bool any = m.T > 0;
+  const size_t need = moe_ws_bytes(m);
+  // the residual last: it may be exactly out's buffer (each value is read by the thread
+  // that then writes it)
+  const Arg in[] = {{"x", x, td, any},           {"router_w", router_w, (size_t)m.E * m.D * 2, true},
+                    {"w_gate", w_gate, w, true}, {"w_up", w_up, w, true},
+                    {"w_down", w_down, w, true}, {"residual", residual, td, false}};
+  const Arg outs[] = {{"out", out, td, any},
+                      {"topk_idx", topk_idx, pairs, false},
+                      {"topk_w", topk_w, pairs, false},
+                      {"workspace", workspace, need, false}};
+  if ((st = check_args(in, 6)) != JM_OK || (st = check_args(outs, 3)) != JM_OK) return st;
+  if ((st = check_workspace("jm_moe_fwd", workspace, ws_bytes, need)) != JM_OK) return st;
+  if ((st = check_disjoint(outs, 4, in, residual == out ? 5 : 6)) != JM_OK) return st;
+  Problem p;
+  begin_call(p, stream);
+  if (!any) {
+    return finish_call(p, cudaMemsetAsync(workspace, 0, sizeof(ErrFlags), p.stream));
+  }
+  m.x = x;
+  m.router_w = router_w;
+  m.w_gate = w_gate;
+  m.w_up = w_up;
+  m.w_down = w_down;
+  m.residual = residual;
+  m.out = out;
+  m.topk_idx = topk_idx;
+  m.topk_w = topk_w;
+  m.ws = static_cast<char*>(workspace);
+  return finish_call(p, run_moe(m, p));
 }

@@ -149,6 +149,25 @@ size_t linear_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, int act);
 cudaError_t run_linear_fwd(const LinearArgs& a, Problem& p);
 cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p);
 
+// The mixture-of-experts layer of k_moe.cu after validation.
+struct MoeArgs {
+  int64_t T, D, F, E, topk;
+  bool topk_softmax;       // weights: softmax over the chosen logits (else over all)
+  const void* x;
+  const void* router_w;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const void* residual;    // may be null
+  void* out;
+  int* topk_idx;           // may be null
+  float* topk_w;           // may be null
+  char* ws;
+};
+bool moe_fits(const MoeArgs& m);       // the sizes' step counts stay below 2^32
+size_t moe_ws_bytes(const MoeArgs& m);
+cudaError_t run_moe(const MoeArgs& m, Problem& p);
+
 // Launch accounting of a call outside the mixer: an empty Problem on `stream`
 // with this thread's timing events, and the status of its end.
 void begin_call(Problem& p, jm_stream_t stream);

@@ -21,6 +21,7 @@
 
 #include <atomic>
 
+#include "block_epilogue.cuh"
 #include "block_math.cuh"
 #include "jmix_internal.cuh"
 #include "sm100.cuh"
@@ -41,14 +42,6 @@ constexpr int stage_bytes(int BN) { return kABytes + b_bytes(BN); }
 constexpr int stages(int BN) { return BN == 256 ? 6 : 8; }
 constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 256; }
 
-struct Epilogue {
-  const __nv_bfloat16* bias;      // [N] or null
-  const __nv_bfloat16* residual;  // [M, N] or null
-  __nv_bfloat16* out;             // [M, N]
-  __nv_bfloat16* pre;             // [M, N] or null
-  int act;
-};
-
 struct PairArgs {
   int64_t M, N, K;
   int64_t m_tiles, n_tiles;
@@ -57,46 +50,6 @@ struct PairArgs {
   Epilogue ep;
   ErrFlags* err;
 };
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-}
-
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-// Bias, activation and residual on 8 consecutive columns of one row, and the stores.
-__device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_t at, int64_t col) {
-  if (e.bias) {
-    float b[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(e.bias + col)), b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += b[j];
-  }
-  if (e.pre) *reinterpret_cast<uint4*>(e.pre + at) = pack8(v);
-  if (e.act != JM_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = act_apply(v[j], e.act);
-  }
-  if (e.residual) {
-    float r[8];
-    unpack8(*reinterpret_cast<const uint4*>(e.residual + at), r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += r[j];
-  }
-  *reinterpret_cast<uint4*>(e.out + at) = pack8(v);
-}
 
 struct Item {
   int64_t mt, nt;
@@ -363,29 +316,9 @@ __global__ void __launch_bounds__(512)
 
 // ------------------------------------------------------------------ host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static std::atomic<EncodeTiledFn> fn{nullptr};
-  EncodeTiledFn f = fn.load(std::memory_order_relaxed);
-  if (!f) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      f = reinterpret_cast<EncodeTiledFn>(p);
-    fn.store(f, std::memory_order_relaxed);
-  }
-  return f;
-}
-
 // A row-major bf16 matrix [outer][inner] as boxes of 64 inner values x `box` rows.
 bool bf16_map(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, int box) {
-  const EncodeTiledFn fn = encode_fn();
+  const EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   cuuint64_t strides[1] = {(cuuint64_t)inner * 2};

@@ -32,7 +32,7 @@ EXPORTED = ("jm_mixer_fwd_workspace_size", "jm_mixer_step_workspace_size", "jm_m
             "jm_noalloc_selftest_timeout", "jm_prepared_weights_size", "jm_prepare_weights",
             "jm_mixer_step_indexed", "jm_norm_fwd", "jm_norm_bwd_workspace_size", "jm_norm_bwd",
             "jm_linear_fwd_workspace_size", "jm_linear_fwd", "jm_linear_bwd_workspace_size",
-            "jm_linear_bwd")
+            "jm_linear_bwd", "jm_moe_fwd_workspace_size", "jm_moe_fwd")
 
 
 class jm_dims(ctypes.Structure):
@@ -52,6 +52,12 @@ class jm_norm_dims(ctypes.Structure):
 class jm_linear_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("in_features", ctypes.c_int64),
                 ("out_features", ctypes.c_int64), ("io", ctypes.c_int), ("act", ctypes.c_int32)]
+
+
+class jm_moe_dims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("d_model", ctypes.c_int64), ("d_ff", ctypes.c_int64),
+                ("n_experts", ctypes.c_int64), ("top_k", ctypes.c_int64), ("io", ctypes.c_int),
+                ("router", ctypes.c_int32)]
 
 
 class JmixError(RuntimeError):
@@ -132,6 +138,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.jm_linear_bwd.restype = ctypes.c_int
     lib.jm_linear_bwd.argtypes = ([ctypes.POINTER(jm_linear_dims)] + [_vp] * 8
                                   + [ctypes.c_size_t, _vp])
+    lib.jm_moe_fwd_workspace_size.restype = ctypes.c_size_t
+    lib.jm_moe_fwd_workspace_size.argtypes = [ctypes.POINTER(jm_moe_dims)]
+    lib.jm_moe_fwd.restype = ctypes.c_int
+    lib.jm_moe_fwd.argtypes = ([ctypes.POINTER(jm_moe_dims)] + [_vp] * 10
+                               + [ctypes.c_size_t, _vp])
     lib.jm_noalloc_poll_error.restype = ctypes.c_int
     lib.jm_noalloc_poll_error.argtypes = [_vp]
     lib.jm_noalloc_selftest_timeout.restype = ctypes.c_int
@@ -172,6 +183,14 @@ JM_ACT_NONE, JM_ACT_RELU, JM_ACT_GELU, JM_ACT_SILU = range(4)
 def linear_dims(rows: int, in_features: int, out_features: int, act: int = JM_ACT_NONE,
                 io: int = JM_BF16) -> jm_linear_dims:
     return jm_linear_dims(rows, in_features, out_features, io, act)
+
+
+JM_ROUTE_SOFTMAX_ALL, JM_ROUTE_SOFTMAX_TOPK = 0, 1
+
+
+def moe_dims(tokens: int, d_model: int, d_ff: int, n_experts: int, top_k: int,
+             router: int = JM_ROUTE_SOFTMAX_ALL, io: int = JM_BF16) -> jm_moe_dims:
+    return jm_moe_dims(tokens, d_model, d_ff, n_experts, top_k, io, router)
 
 
 def _ptr(t) -> Optional[int]:
@@ -347,6 +366,21 @@ def jm_linear_bwd(d: jm_linear_dims, g_out, x, w, workspace, ws_bytes: int, pre=
     """Backward of jm_linear_fwd (see include/jmix.h)."""
     p = _tensors(d.io, g_out=g_out, x=x, w=w, pre=pre, g_x=g_x, g_w=g_w, g_bias=g_bias)
     st = load().jm_linear_bwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
+    if check:
+        _check(st)
+    return st
+
+
+def jm_moe_fwd_workspace_size(d: jm_moe_dims) -> int:
+    return load().jm_moe_fwd_workspace_size(ctypes.byref(d))
+
+
+def jm_moe_fwd(d: jm_moe_dims, x, router_w, w_gate, w_up, w_down, out, workspace, ws_bytes: int,
+               residual=None, topk_idx=None, topk_w=None, stream=None, check: bool = True) -> int:
+    """Mixture-of-experts layer for few tokens (see include/jmix.h)."""
+    p = _tensors(d.io, x=x, router_w=router_w, w_gate=w_gate, w_up=w_up, w_down=w_down,
+                 residual=residual, out=out, topk_idx_i32=topk_idx, topk_w_f32=topk_w)
+    st = load().jm_moe_fwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
     if check:
         _check(st)
     return st

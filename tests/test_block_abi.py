@@ -170,3 +170,55 @@ def test_linear_rejects_bad_pointers():
     assert linear_bwd(d, pre=p, g_x=F + G) == bad and "g_x overlaps x" in jmix.jm_last_error()
     assert linear_bwd(d, pre=p, g_w=F + 3 * G) == bad
     assert linear_bwd(d, pre=p, nbytes=255) == jmix.JM_ERR_WORKSPACE
+
+
+def moe_fwd(d, nbytes=None, **over):
+    a = dict(x=F, router_w=F + G, w_gate=F + 2 * G, w_up=F + 3 * G, w_down=F + 4 * G,
+             out=F + 5 * G, workspace=W,
+             ws_bytes=jmix.jm_moe_fwd_workspace_size(d) if nbytes is None else nbytes)
+    a.update(over)
+    return jmix.jm_moe_fwd(d, **a, stream=0, check=False)
+
+
+@pytest.mark.parametrize("over,code,msg", [
+    (dict(tokens=-1), jmix.JM_ERR_INVALID_ARG, "positive"),
+    (dict(d_model=0), jmix.JM_ERR_INVALID_ARG, "positive"),
+    (dict(top_k=0), jmix.JM_ERR_INVALID_ARG, "positive"),
+    (dict(d_model=60), jmix.JM_ERR_INVALID_ARG, "multiples of 8"),
+    (dict(d_ff=12), jmix.JM_ERR_INVALID_ARG, "multiples of 8"),
+    (dict(top_k=5), jmix.JM_ERR_INVALID_ARG, "n_experts"),
+    (dict(tokens=257), jmix.JM_ERR_UNSUPPORTED, "256 tokens"),
+    (dict(n_experts=257), jmix.JM_ERR_UNSUPPORTED, "experts"),
+    (dict(n_experts=16, top_k=9), jmix.JM_ERR_UNSUPPORTED, "top_k"),
+    (dict(io=jmix.JM_F32), jmix.JM_ERR_UNSUPPORTED, "bf16"),
+    (dict(io=9), jmix.JM_ERR_INVALID_ARG, "io dtype"),
+    (dict(router=2), jmix.JM_ERR_INVALID_ARG, "router"),
+    (dict(d_model=1 << 24, d_ff=1 << 24), jmix.JM_ERR_INVALID_ARG, "large"),
+])
+def test_moe_rejects_bad_dims(over, code, msg):
+    kw = dict(tokens=4, d_model=64, d_ff=128, n_experts=4, top_k=2)
+    kw.update(over)
+    d = jmix.moe_dims(**kw)
+    assert moe_fwd(d, 1 << 30) == code and msg in jmix.jm_last_error()
+    assert jmix.jm_moe_fwd_workspace_size(d) == 0
+
+
+def test_moe_rejects_bad_pointers():
+    bad = jmix.JM_ERR_INVALID_ARG
+    d = jmix.moe_dims(4, 64, 128, 4, 2)
+    for k in ("x", "router_w", "w_gate", "w_up", "w_down", "out"):
+        assert moe_fwd(d, **{k: None}) == bad and "NULL" in jmix.jm_last_error(), k
+        assert moe_fwd(d, **{k: F + 8}) == bad and "aligned" in jmix.jm_last_error(), k
+    assert moe_fwd(d, out=F) == bad and "out overlaps x" in jmix.jm_last_error()
+    assert moe_fwd(d, residual=F + 5 * G + 64) == bad
+    assert "out overlaps residual" in jmix.jm_last_error()
+    assert moe_fwd(d, topk_idx=F + 5 * G) == bad and "topk_idx overlaps out" in jmix.jm_last_error()
+    assert moe_fwd(d, topk_w=F + 2 * G) == bad and "topk_w overlaps w_gate" in jmix.jm_last_error()
+    assert moe_fwd(d, workspace=F + 4 * G) == bad
+    # the residual in out's place, but a list over it is not
+    r = F + 5 * G
+    assert moe_fwd(d, residual=r, topk_idx=r) == bad
+    n = jmix.jm_moe_fwd_workspace_size(d)
+    assert moe_fwd(d, nbytes=n - 1) == jmix.JM_ERR_WORKSPACE
+    assert moe_fwd(d, workspace=None) == jmix.JM_ERR_WORKSPACE
+    assert moe_fwd(d, workspace=W + 64) == jmix.JM_ERR_WORKSPACE
