@@ -286,46 +286,83 @@ def jm_scan_bwd(d: jm_dims, delta, u, Bm, Cm, A_log, D, h0, gy, g_delta, g_u, g_
     return st
 
 
-def _tensors(io: int, **named):
-    """Addresses of the named tensors.  A torch tensor's layout and type cannot be read
-    from its address, so they are checked here: on the current device, of the call's io
-    type (names ending in ``_f32`` float32, in ``_i32`` int32), contiguous (names ending in
-    ``_rows``: contiguous within a row; its stride is the dims' business)."""
-    out = []
-    for name, t in named.items():
-        if t is None or isinstance(t, int):
-            out.append(t)
+# What a call's arguments are: of the io type, float32, int32, of the io type with the row
+# stride in the dims, or bytes of any type.
+_IO, _F32, _I32, _ROWS, _RAW = range(5)
+_types = None      # torch dtypes by kind for JM_F32 and JM_BF16, once torch is imported
+_raw_stream = None
+
+
+def _use_torch() -> None:
+    global _types, _raw_stream
+    import torch
+    f, i, b = torch.float32, torch.int32, torch.bfloat16
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _types = {JM_F32: (f, f, i, f), JM_BF16: (b, f, i, b)}
+
+
+def _bad(msg: str):
+    raise JmixError(JM_ERR_INVALID_ARG, msg)
+
+
+def _call(fn, d, spec, tensors, tail=(), stream=None, check: bool = True) -> int:
+    """fn(d, addresses of `tensors`, *tail, stream).  A tensor's layout, type and device
+    cannot be read from its address, so they are checked here against `spec`, a tuple of
+    (name, kind).  (A decode step's operators take microseconds: this path is kept short.)"""
+    if _types is None:
+        _use_torch()
+    types, dev, args = _types.get(d.io, _types[JM_BF16]), -1, []
+    for (name, kind), t in zip(spec, tensors):
+        if t is None or type(t) is int:
+            args.append(t)
             continue
-        import torch
-        want = torch.bfloat16 if io == JM_BF16 else torch.float32
-        ok = t.is_contiguous()
-        base, _, tag = name.rpartition("_")
-        if tag == "f32":
-            name, want = base, torch.float32
-        elif tag == "i32":
-            name, want = base, torch.int32
-        elif tag == "rows":
-            name, ok = base, t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1
-        if t.dtype != want:
-            raise JmixError(JM_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call needs {want}")
-        if not ok:
-            raise JmixError(JM_ERR_INVALID_ARG, f"{name} is not contiguous")
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            raise JmixError(JM_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current "
-                                                "CUDA device")
-        out.append(t.data_ptr())
-    return out
+        if kind != _RAW and t.dtype is not types[kind]:
+            _bad(f"{name} is {t.dtype}, the call needs {types[kind]}")
+        if not t.is_contiguous():
+            if kind != _ROWS or t.shape[-1] > 1 and t.stride(-1) != 1:
+                _bad(f"{name} is not contiguous")
+            if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != d.x_stride:
+                _bad(f"{name} has row stride {t.stride(0)}, the dims say {d.x_stride}")
+        at = t.get_device()
+        if at != dev or at < 0:
+            if at >= 0 and dev < 0:
+                import torch
+                dev = torch.cuda.current_device()
+            if at != dev or at < 0:
+                _bad(f"{name} is on {t.device}, not on the current CUDA device")
+        args.append(t.data_ptr())
+    if stream is None:
+        if dev < 0:
+            import torch
+            dev = torch.cuda.current_device()
+        stream = _raw_stream(dev)
+    elif type(stream) is not int:
+        stream = stream.cuda_stream
+    st = fn(ctypes.byref(d), *args, *tail, stream)
+    if check and st != JM_OK:
+        _check(st)
+    return st
+
+
+def _spec(names: str, **kinds):
+    return tuple((n, kinds.get(n, _IO)) for n in names.split())
+
+
+_NORM_FWD = _spec("x residual weight bias y sum stats", x=_ROWS, stats=_F32)
+_NORM_BWD = _spec("g_y x weight stats g_sum g_x g_weight g_bias workspace", x=_ROWS, stats=_F32,
+                  workspace=_RAW)
+_LINEAR_FWD = _spec("x w bias residual out pre workspace", workspace=_RAW)
+_LINEAR_BWD = _spec("g_out x w pre g_x g_w g_bias workspace", workspace=_RAW)
+_MOE_FWD = _spec("x router_w w_gate w_up w_down residual out topk_idx topk_w workspace",
+                 topk_idx=_I32, topk_w=_F32, workspace=_RAW)
 
 
 def jm_norm_fwd(d: jm_norm_dims, x, weight, y, bias=None, residual=None, sum_out=None, stats=None,
                 stream=None, check: bool = True) -> int:
     """Residual add and LayerNorm / RMSNorm of each row (see include/jmix.h)."""
-    p = _tensors(d.io, x_rows=x, residual=residual, weight=weight, bias=bias, y=y, sum=sum_out,
-                 stats_f32=stats)
-    st = load().jm_norm_fwd(ctypes.byref(d), *p, _stream(stream))
-    if check:
-        _check(st)
-    return st
+    return _call(load().jm_norm_fwd, d, _NORM_FWD,
+                 (x, residual, weight, bias, y, sum_out, stats), (), stream, check)
 
 
 def jm_norm_bwd_workspace_size(d: jm_norm_dims) -> int:
@@ -335,12 +372,9 @@ def jm_norm_bwd_workspace_size(d: jm_norm_dims) -> int:
 def jm_norm_bwd(d: jm_norm_dims, g_y, x, weight, stats, g_x, workspace, ws_bytes: int, g_sum=None,
                 g_weight=None, g_bias=None, stream=None, check: bool = True) -> int:
     """Backward of jm_norm_fwd (see include/jmix.h); x is the forward's sum, or its x."""
-    p = _tensors(d.io, g_y=g_y, x_rows=x, weight=weight, stats_f32=stats, g_sum=g_sum, g_x=g_x,
-                 g_weight=g_weight, g_bias=g_bias)
-    st = load().jm_norm_bwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
-    if check:
-        _check(st)
-    return st
+    return _call(load().jm_norm_bwd, d, _NORM_BWD,
+                 (g_y, x, weight, stats, g_sum, g_x, g_weight, g_bias, workspace), (ws_bytes,),
+                 stream, check)
 
 
 def jm_linear_fwd_workspace_size(d: jm_linear_dims) -> int:
@@ -350,11 +384,8 @@ def jm_linear_fwd_workspace_size(d: jm_linear_dims) -> int:
 def jm_linear_fwd(d: jm_linear_dims, x, w, out, workspace, ws_bytes: int, bias=None, residual=None,
                   pre=None, stream=None, check: bool = True) -> int:
     """out = act(x . w^T + bias) + residual (see include/jmix.h)."""
-    p = _tensors(d.io, x=x, w=w, bias=bias, residual=residual, out=out, pre=pre)
-    st = load().jm_linear_fwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
-    if check:
-        _check(st)
-    return st
+    return _call(load().jm_linear_fwd, d, _LINEAR_FWD,
+                 (x, w, bias, residual, out, pre, workspace), (ws_bytes,), stream, check)
 
 
 def jm_linear_bwd_workspace_size(d: jm_linear_dims) -> int:
@@ -364,11 +395,8 @@ def jm_linear_bwd_workspace_size(d: jm_linear_dims) -> int:
 def jm_linear_bwd(d: jm_linear_dims, g_out, x, w, workspace, ws_bytes: int, pre=None, g_x=None,
                   g_w=None, g_bias=None, stream=None, check: bool = True) -> int:
     """Backward of jm_linear_fwd (see include/jmix.h)."""
-    p = _tensors(d.io, g_out=g_out, x=x, w=w, pre=pre, g_x=g_x, g_w=g_w, g_bias=g_bias)
-    st = load().jm_linear_bwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
-    if check:
-        _check(st)
-    return st
+    return _call(load().jm_linear_bwd, d, _LINEAR_BWD,
+                 (g_out, x, w, pre, g_x, g_w, g_bias, workspace), (ws_bytes,), stream, check)
 
 
 def jm_moe_fwd_workspace_size(d: jm_moe_dims) -> int:
@@ -378,12 +406,9 @@ def jm_moe_fwd_workspace_size(d: jm_moe_dims) -> int:
 def jm_moe_fwd(d: jm_moe_dims, x, router_w, w_gate, w_up, w_down, out, workspace, ws_bytes: int,
                residual=None, topk_idx=None, topk_w=None, stream=None, check: bool = True) -> int:
     """Mixture-of-experts layer for few tokens (see include/jmix.h)."""
-    p = _tensors(d.io, x=x, router_w=router_w, w_gate=w_gate, w_up=w_up, w_down=w_down,
-                 residual=residual, out=out, topk_idx_i32=topk_idx, topk_w_f32=topk_w)
-    st = load().jm_moe_fwd(ctypes.byref(d), *p, _ptr(workspace), ws_bytes, _stream(stream))
-    if check:
-        _check(st)
-    return st
+    return _call(load().jm_moe_fwd, d, _MOE_FWD,
+                 (x, router_w, w_gate, w_up, w_down, residual, out, topk_idx, topk_w, workspace),
+                 (ws_bytes,), stream, check)
 
 
 def jm_selftest_timeout(workspace, ws_bytes: int, stream=None, check: bool = True) -> int:
