@@ -14,7 +14,11 @@
 // k_linear_pair: persistent CTA pairs (cluster of 2, cta_group::2), a 256 x BN tile
 // per pair, 64-wide K chunks in a TMA ring, the leader issues the MMAs, each CTA
 // drains its 128 rows from one of two accumulators while the next tile fills the
-// other.  Problems with few tiles are cut along K (`splits`): the work items write
+// other.  Eight warps drain: a tile of 256 x 256 takes the tensor cores 17 us at K 4096
+// but 7 us at K 1744, and one warp for each quarter of the TMEM lanes needed 20 us with
+// an activation (6063 x 1744 x 8952 with SiLU: 322 us).  They stage 64 columns at a time
+// in swizzled shared memory; the residual comes into the same place by TMA before the
+// accumulator is complete, and TMA stores write whole lines.  Problems with few tiles are cut along K (`splits`): the work items write
 // float32 partial tiles and k_linear_reduce adds them in a fixed order and applies
 // the epilogue.
 #include <cuda.h>
@@ -33,23 +37,47 @@ using namespace sm100;
 
 constexpr int kK = 64;              // K chunk: one 128-byte swizzle atom of bf16
 constexpr int kHalf = 128;          // tile rows per CTA
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;      // producer, MMA and 8 epilogue warps
+constexpr int kOutBytes = kHalf * 128;  // an epilogue group's staging: 128 rows x 128 bytes
 constexpr int kGroupM = 16;         // row tiles per raster group
 constexpr uint32_t kTmemCols = 512;
 constexpr int kABytes = kHalf * kK * 2;                      // 16 KB
 constexpr int b_bytes(int BN) { return BN / 2 * kK * 2; }    // 16 or 8 KB
 constexpr int stage_bytes(int BN) { return kABytes + b_bytes(BN); }
-constexpr int stages(int BN) { return BN == 256 ? 6 : 8; }
-constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 256; }
+constexpr int stages(int BN) { return BN == 256 ? 6 : 7; }
+constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 2 * kOutBytes + 256; }
 
 struct PairArgs {
   int64_t M, N, K;
   int64_t m_tiles, n_tiles;
-  int splits;
-  float* part;   // [splits][M][N] when splits > 1
-  Epilogue ep;
+  int splits;    // above 1: float32 partial tiles [splits][M][N] through tm_out
+  Epilogue ep;   // (its out and residual are reached through the maps)
   ErrFlags* err;
+  bool clear_err;  // the first kernel of a call clears the error header
 };
+
+__device__ __forceinline__ void group_sync(int grp) {
+  asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
+}
+
+__device__ __forceinline__ uint4 pack8_bits(const uint32_t* v) {
+  return make_uint4(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                    pack2(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                    pack2(__uint_as_float(v[4]), __uint_as_float(v[5])),
+                    pack2(__uint_as_float(v[6]), __uint_as_float(v[7])));
+}
+
+template <int ACT>
+__device__ __forceinline__ void apply_one(uint32_t (&v)[64]) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(act_apply(__uint_as_float(v[i]), ACT));
+}
+
+__device__ __forceinline__ void apply_act(uint32_t (&v)[64], int act) {
+  if (act == JM_ACT_RELU) apply_one<JM_ACT_RELU>(v);
+  if (act == JM_ACT_GELU) apply_one<JM_ACT_GELU>(v);
+  if (act == JM_ACT_SILU) apply_one<JM_ACT_SILU>(v);
+}
 
 struct Item {
   int64_t mt, nt;
@@ -75,16 +103,20 @@ __device__ __forceinline__ Item item_of(const PairArgs& g, int64_t w, int kchunk
 template <bool AMN, bool BMN, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                  const PairArgs g) {
+                  const __grid_constant__ CUtensorMap tm_out,
+                  const __grid_constant__ CUtensorMap tm_res,
+                  const __grid_constant__ CUtensorMap tm_pre, const PairArgs g) {
   constexpr int S = stages(BN), kStage = stage_bytes(BN), kBHalf = BN / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kStage);
+  uint8_t* staging = smem + S * kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 2 * kOutBytes);
   uint64_t* full = bars;              // [S] (leader) both CTAs' halves landed
   uint64_t* empty = bars + S;         // [S] the pair's MMAs have read the stage
   uint64_t* acc_full = bars + 2 * S;  // [2] accumulator complete
-  uint64_t* acc_empty = acc_full + 2; // [2] (leader) both epilogues are done (8 warps)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* acc_empty = acc_full + 2; // [2] (leader) both epilogues are done (16 warps)
+  uint64_t* res_full = acc_empty + 2; // [2] a group's residual box landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -100,7 +132,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 8);
+      mbar_init(smem_u32(&acc_empty[b]), 16);
+      mbar_init(smem_u32(&res_full[b]), 1);
     }
     fence_mbar_init();
   }
@@ -111,12 +144,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_a);
     prefetch_tmap(&tm_b);
+    prefetch_tmap(&tm_out);
   }
   tc_fence_before();
   cluster_sync();   // both CTAs' barriers exist before either signals the other's
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
+  grid_dep_launch();
+  // (a wait gives up after 2 s: no CTA can have recorded one yet)
+  if (g.clear_err && blockIdx.x == 0 && threadIdx.x < sizeof(ErrFlags) / 4)
+    reinterpret_cast<unsigned*>(g.err)[threadIdx.x] = 0u;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -187,48 +225,119 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // epilogue: this CTA's 128 rows of the pair's 256-row tile, a row per thread
-    const int lg = warp & 3;
+    // epilogue: this CTA's 128 rows of the pair's 256-row tile, a row per thread; two
+    // groups of 4 warps take the 128-byte column chunks in turn
+    const int lg = warp & 3, grp = (warp - 2) >> 2, r = lg * 32 + lane;
+    const bool first = r == 0;
+    const bool split = g.splits > 1, act = g.ep.act != JM_ACT_NONE;
+    const int cw = split ? 32 : 64;                   // columns in 128 bytes
     const uint32_t acc_empty_leader = leader_addr(smem_u32(&acc_empty[0]));
+    uint8_t* stage = staging + grp * kOutBytes;
+    uint4* mine = reinterpret_cast<uint4*>(stage + r * 128);
+    const int sw = r & 7;                             // the swizzle of this row
+    const uint32_t res_bar = smem_u32(&res_full[grp]);
+    uint32_t res_phase = 0;
     int64_t j = 0;
+    // (a thread whose wait ran out goes on without waiting, so that its group's barriers
+    // stay matched; the error header says that the values are not to be used)
+    bool ok = true;
     for (int64_t w = pair; w < items; w += npairs, ++j) {
       const Item q = item_of(g, w, kchunks);
       const int b = (int)(j & 1);
-      if (!mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(j >> 1) & 1u, g.err, 84)) break;
-      tc_fence_after();
-      const int64_t row = q.mt * (2 * kHalf) + rank * kHalf + lg * 32 + lane;
-      const int64_t n0 = q.nt * BN;
+      const int64_t row0 = q.mt * (2 * kHalf) + rank * kHalf, n0 = q.nt * BN;
+      const bool rows = row0 < g.M;
       const uint32_t tbase = tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(b * 256);
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        if (n0 + c >= g.N) break;
-        uint32_t r[32];
-        tmem_ld16(tbase + (uint32_t)c, *reinterpret_cast<uint32_t(*)[16]>(r));
-        tmem_ld16(tbase + (uint32_t)(c + 16), *reinterpret_cast<uint32_t(*)[16]>(r + 16));
-        tmem_ld_wait();
-        if (row < g.M) {
-#pragma unroll
-          for (int o = 0; o < 4; ++o) {  // 8 columns at a time
-            const int64_t col = n0 + c + 8 * o;
-            if (col + 8 > g.N) break;
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * o + i]);
-            const int64_t at = row * g.N + col;
-            if (g.splits > 1) {
-              float4* dst = reinterpret_cast<float4*>(g.part + (int64_t)q.split * g.M * g.N + at);
-              dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-              dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-              finish8(g.ep, v, at, col);
-            }
+      bool waited = false;
+      for (int c = grp * cw; rows && c < BN && n0 + c < g.N; c += 2 * cw) {
+        const int64_t col = n0 + c;
+        if (first) {
+          bulk_wait_read<0>();   // the staging is free
+          if (ok && !split && g.ep.residual) {
+            mbar_arrive_expect_tx(res_bar, kOutBytes);
+            tma_load_2d(smem_u32(stage), &tm_res, res_bar, (int32_t)col, (int32_t)row0);
           }
         }
+        group_sync(grp);
+        if (!waited) ok = ok && mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(j >> 1) & 1u, g.err, 84);
+        waited = true;
+        tc_fence_after();
+        uint32_t v[64];
+        if (split) {
+          tmem_ld16(tbase + c, *reinterpret_cast<uint32_t(*)[16]>(v));
+          tmem_ld16(tbase + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            mine[i ^ sw] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tmem_ld16(tbase + c + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(v + 16 * i));
+          tmem_ld_wait();
+          uint4 res[8];
+          if (g.ep.residual) {
+            ok = ok && mbar_wait(res_bar, res_phase, g.err, 85);
+            res_phase ^= 1u;
+            if (g.ep.pre)   // the staging holds pre first
+#pragma unroll
+              for (int i = 0; i < 8; ++i) res[i] = mine[i ^ sw];
+          }
+          if (g.ep.bias) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (col + 8 * i < g.N) {
+                float bv[8];
+                unpack8(__ldg(reinterpret_cast<const uint4*>(g.ep.bias + col) + i), bv);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  v[8 * i + k] = __float_as_uint(__uint_as_float(v[8 * i + k]) + bv[k]);
+              }
+            }
+          }
+          if (g.ep.pre) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mine[i ^ sw] = pack8_bits(v + 8 * i);
+            fence_proxy_async_smem();
+            group_sync(grp);
+            if (first) {
+              tma_store_2d(&tm_pre, smem_u32(stage), (int32_t)col, (int32_t)row0);
+              bulk_commit();
+              bulk_wait_read<0>();
+            }
+            group_sync(grp);
+          }
+          if (act) {
+            apply_act(v, g.ep.act);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (g.ep.residual) {
+              float rv[8];
+              unpack8(g.ep.pre ? res[i] : mine[i ^ sw], rv);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                v[8 * i + k] = __float_as_uint(__uint_as_float(v[8 * i + k]) + rv[k]);
+            }
+            mine[i ^ sw] = pack8_bits(v + 8 * i);
+          }
+        }
+        fence_proxy_async_smem();
+        group_sync(grp);
+        if (first) {
+          if (split)
+            tma_store_3d(&tm_out, smem_u32(stage), (int32_t)col, (int32_t)row0, q.split);
+          else
+            tma_store_2d(&tm_out, smem_u32(stage), (int32_t)col, (int32_t)row0);
+          bulk_commit();
+        }
       }
+      // the accumulator is free once it is complete and this warp has read its part
+      if (!waited) ok = ok && mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(j >> 1) & 1u, g.err, 84);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty_leader + (uint32_t)(b * 8));
     }
+    if (first) bulk_wait_all();
   }
   tc_fence_before();
   cluster_sync();   // no CTA leaves while its pair may still signal it
@@ -243,6 +352,7 @@ __global__ void __launch_bounds__(256)
     k_linear_reduce(const float* __restrict__ part, int splits, int64_t M, int64_t N,
                     const Epilogue ep) {
   grid_dep_wait();
+  grid_dep_launch();
   const int64_t n8 = N / 8, total = M * n8;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
@@ -268,6 +378,7 @@ __global__ void __launch_bounds__(256)
                   int act, int64_t M, int64_t N, int rows, __nv_bfloat16* __restrict__ gp,
                   float* __restrict__ part, ErrFlags* err) {
   grid_dep_wait();
+  grid_dep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(ErrFlags) / 4)
     reinterpret_cast<unsigned*>(err)[threadIdx.x] = 0u;
   const int64_t col = (int64_t)blockIdx.x * kGpCols + threadIdx.x * 8;
@@ -301,6 +412,7 @@ __global__ void __launch_bounds__(512)
                          __nv_bfloat16* __restrict__ g_bias) {
   __shared__ float sh[16][33];
   grid_dep_wait();
+  grid_dep_launch();
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float acc = 0.0f;
   if (c < N)
@@ -324,6 +436,19 @@ bool bf16_map(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, in
   cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
   cuuint32_t bx[2] = {(cuuint32_t)kK, (cuuint32_t)box}, es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Partial tiles [splits][M][N], float32, as boxes of 32 columns x 128 rows.
+bool part_map(CUtensorMap* m, const void* base, int64_t splits, int64_t M, int64_t N) {
+  const EncodeTiledFn fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)splits};
+  cuuint64_t strides[2] = {(cuuint64_t)N * 4, (cuuint64_t)(M * N) * 4};
+  cuuint32_t bx[3] = {32, kHalf, 1}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, bx, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -404,8 +529,7 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, c
 }
 
 template <bool AMN, bool BMN, int BN>
-cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const PairArgs& g,
-                        cudaStream_t s) {
+cudaError_t launch_pair(const CUtensorMap (&tm)[5], const PairArgs& g, cudaStream_t s) {
   static std::atomic<int> cache[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -415,17 +539,22 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const Pair
   const int64_t items = g.m_tiles * g.n_tiles * g.splits;
   const int64_t pairs = items < most ? items : most;
   return launch(k_linear_pair<AMN, BMN, BN>, dim3((unsigned)(2 * pairs)), dim3(kThreads),
-                (size_t)smem_bytes(BN), s, ta, tb, g);
+                (size_t)smem_bytes(BN), s, tm[0], tm[1], tm[2], tm[3], tm[4], g);
 }
 
 // C[M, N] = A . B^T with the epilogue `ep`.  AMN / BMN: A is stored [K, M], B [K, N].
 template <bool AMN, bool BMN>
 cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* B,
-                    const Epilogue& ep, float* part, ErrFlags* err, Problem& p) {
+                    const Epilogue& ep, float* part, ErrFlags* err, bool clear_err, Problem& p) {
   const Cut c = choose_cut(M, N, K);
-  CUtensorMap ta, tb;
-  const bool ok = (AMN ? bf16_map(&ta, A, K, M, 64) : bf16_map(&ta, A, M, K, kHalf)) &&
-                  (BMN ? bf16_map(&tb, B, K, N, 64) : bf16_map(&tb, B, N, K, c.bn / 2));
+  CUtensorMap tm[5];
+  bool ok = (AMN ? bf16_map(&tm[0], A, K, M, 64) : bf16_map(&tm[0], A, M, K, kHalf)) &&
+            (BMN ? bf16_map(&tm[1], B, K, N, 64) : bf16_map(&tm[1], B, N, K, c.bn / 2)) &&
+            (c.splits > 1 ? part_map(&tm[2], part, c.splits, M, N)
+                          : bf16_map(&tm[2], ep.out, M, N, kHalf));
+  tm[3] = tm[4] = tm[2];
+  if (ep.residual) ok = ok && bf16_map(&tm[3], ep.residual, M, N, kHalf);
+  if (ep.pre) ok = ok && bf16_map(&tm[4], ep.pre, M, N, kHalf);
   if (!ok) return cudaErrorInvalidValue;
   PairArgs g{};
   g.M = M;
@@ -434,11 +563,11 @@ cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* 
   g.m_tiles = (M + 255) / 256;
   g.n_tiles = (N + c.bn - 1) / c.bn;
   g.splits = c.splits;
-  g.part = part;
   g.ep = ep;
   g.err = err;
-  cudaError_t e = c.bn == 256 ? launch_pair<AMN, BMN, 256>(ta, tb, g, p.stream)
-                              : launch_pair<AMN, BMN, 128>(ta, tb, g, p.stream);
+  g.clear_err = clear_err;
+  cudaError_t e = c.bn == 256 ? launch_pair<AMN, BMN, 256>(tm, g, p.stream)
+                              : launch_pair<AMN, BMN, 128>(tm, g, p.stream);
   if (e != cudaSuccess) return e;
   launched(p, "k_linear_pair");
   if (c.splits > 1) {
@@ -498,8 +627,7 @@ size_t linear_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
 
 cudaError_t run_linear_fwd(const LinearArgs& a, Problem& p) {
   ErrFlags* err = reinterpret_cast<ErrFlags*>(a.ws);
-  cudaError_t e = cudaMemsetAsync(err, 0, sizeof(ErrFlags), p.stream);
-  if (e != cudaSuccess || a.M == 0) return e;
+  if (a.M == 0) return cudaMemsetAsync(err, 0, sizeof(ErrFlags), p.stream);
   Epilogue ep{};
   ep.bias = static_cast<const __nv_bfloat16*>(a.bias);
   ep.residual = static_cast<const __nv_bfloat16*>(a.residual);
@@ -508,7 +636,7 @@ cudaError_t run_linear_fwd(const LinearArgs& a, Problem& p) {
   ep.act = a.act;
   launches_begin(p);
   return product<false, false>(a.M, a.N, a.K, a.x, a.w, ep,
-                               reinterpret_cast<float*>(a.ws + sizeof(ErrFlags)), err, p);
+                               reinterpret_cast<float*>(a.ws + sizeof(ErrFlags)), err, true, p);
 }
 
 cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
@@ -541,20 +669,21 @@ cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
       if (e != cudaSuccess) return e;
       launched(p, "k_linear_bias_reduce");
     }
-  } else {
-    e = cudaMemsetAsync(err, 0, sizeof(ErrFlags), p.stream);
-    if (e != cudaSuccess) return e;
+  } else if (!a.g_x && !a.g_w) {
+    return cudaMemsetAsync(err, 0, sizeof(ErrFlags), p.stream);
   }
+  const bool clear = !grad && !a.g_bias;   // else k_linear_gpre has done it
   Epilogue ep{};
   ep.act = JM_ACT_NONE;
   if (a.g_x) {  // [M, K] = g_p [M, N] . w [N, K]
     ep.out = static_cast<__nv_bfloat16*>(a.g_x);
-    e = product<false, true>(a.M, a.K, a.N, gp, a.w, ep, w.part, err, p);
+    e = product<false, true>(a.M, a.K, a.N, gp, a.w, ep, w.part, err, clear, p);
     if (e != cudaSuccess) return e;
   }
   if (a.g_w) {  // [N, K] = g_p [M, N]^T . x [M, K]
     ep.out = static_cast<__nv_bfloat16*>(a.g_w);
-    e = product<true, true>(a.N, a.K, a.M, gp, a.x, ep, w.part, err, p);
+    e = product<true, true>(a.N, a.K, a.M, gp, a.x, ep, w.part, err, clear && !a.g_x,
+                            p);
   }
   return e;
 }

@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const MoeKArgs a) {
   __shared__ double logits[kMaxExperts];
   const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
+  grid_dep_launch();
   if (t == 0) {
     unsigned* s = reinterpret_cast<unsigned*>(a.sync);
     for (unsigned i = threadIdx.x; i < sizeof(Sync) / 4; i += kRouteThreads) s[i] = 0u;

@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(MAXT) k_norm_fwd(const NormFwdArgs a) {
   const bool live = row < a.rows;
   const int nvec = (int)(a.cols / VEC);
   grid_dep_wait();
+  grid_dep_launch();
   const R* x = reinterpret_cast<const R*>(static_cast<const T*>(a.x) + (live ? row : 0) * a.x_stride);
   const int64_t base = (live ? row : 0) * (int64_t)nvec;
   const R* res = a.residual ? static_cast<const R*>(a.residual) + base : nullptr;
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) k_norm_bwd(const No
   const int64_t step = (int64_t)gridDim.x * a.rpc;
   const int64_t first = (int64_t)blockIdx.x * a.rpc + group;
   grid_dep_wait();
+  grid_dep_launch();
   if (blockIdx.x == 0 && threadIdx.x < sizeof(ErrFlags) / 4)
     reinterpret_cast<unsigned*>(a.err)[threadIdx.x] = 0u;
   const R* wp = static_cast<const R*>(a.weight);
@@ -312,7 +314,6 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) k_norm_bwd(const No
       }
     }
   }
-  grid_dep_launch();
 }
 
 // g_w (blockIdx.y = 0) and g_b (1): the partial rows of 32 columns, added in a
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(32 * kRedRows)
   T* out = blockIdx.y == 0 ? g_w : g_b;
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   grid_dep_wait();
+  grid_dep_launch();
   if (!out) return;
   float acc = 0.0f;
   if (c < cols) {
@@ -426,7 +428,7 @@ cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p) {
   a.wpr = s.wpr;
   a.rpc = s.rpc;
   const int64_t ctas = (a.rows + s.rpc - 1) / s.rpc;
-    launches_begin(p);
+  launches_begin(p);
   const cudaError_t e = launch_pdl(fwd_kernel(s, io), dim3((unsigned)ctas), dim3(s.threads()),
                                    p.stream, a);
   if (e == cudaSuccess) launched(p, "k_norm_fwd");
