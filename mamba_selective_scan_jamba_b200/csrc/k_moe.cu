@@ -64,6 +64,7 @@ struct Lists {
   uint16_t row[kMaxPairs];       // pair row of token * top_k + choice
   int count[kMaxExperts];
   int first[kMaxExperts];        // first pair row of an expert
+  uint16_t block[kMaxExperts];   // first block of an expert
   int n_entries;
 };
 
@@ -91,26 +92,57 @@ struct MoeKArgs {
   ErrFlags* err;
 };
 
-// A phase's line of work, cut between `ctas` CTAs.
+// A phase's line of work: `parts` parts of `quant` steps, cut between `ctas` CTAs.
 struct Line {
-  unsigned tiles, ksteps, total, ctas;
+  unsigned tiles, ksteps, total, quant, parts, ctas;
+  double inv;   // 1 / parts
   __device__ __forceinline__ unsigned start(unsigned c) const {
-    return (unsigned)((uint64_t)total * min(c, ctas) / ctas);
+    return (unsigned)((uint64_t)parts * min(c, ctas) / ctas) * quant;
   }
-  // the CTA whose range holds step s (total * ctas < 2^32, checked on the host)
-  __device__ __forceinline__ unsigned cta_of(unsigned s) const {
-    return ((s + 1) * ctas - 1) / total;
+  // the CTA whose range holds the part p: ((p + 1) ctas - 1) / parts (below 2^32, checked
+  // on the host; by a multiplication, which may be one off)
+  __device__ __forceinline__ unsigned cta_of_part(unsigned p) const {
+    const unsigned x = (p + 1) * ctas - 1;
+    unsigned q = (unsigned)((double)x * inv);
+    const int r = (int)(x - q * parts);
+    if (r < 0) --q;
+    if (r >= (int)parts) ++q;
+    return q;
+  }
+  // the first and the last CTA of a unit
+  __device__ __forceinline__ void ctas_of(unsigned unit, unsigned& c0, unsigned& c1) const {
+    if (quant > 1) {   // whole units
+      c0 = c1 = cta_of_part(unit);
+    } else {
+      c0 = cta_of_part(unit * ksteps);
+      c1 = cta_of_part((unit + 1) * ksteps - 1);
+    }
   }
 };
 
-// No more CTAs than steps, so that no range between two others is empty.
+// Whole units or ranges cut anywhere?  Cut ranges give every CTA the same bytes, but
+// their partial tiles cost `join_us`.  Whole units leave the last round's CTAs to
+// themselves, and one SM's loads from HBM reach about 60 GB/s: a step of 32 KB takes the
+// whole GPU 5 ns, but one SM 550 ns.  Measured: one token, 2 of 16 experts of 4096 x 14336
+// (224 units of 64 steps), cut 128 us, whole 136 us; 13 tokens, 8 experts of 512 x 1416
+// (96 units of 8 steps), cut 34 us, whole 27 us.  There are no more CTAs than parts, so
+// that no range between two others is empty.
 __device__ __forceinline__ Line make_line(unsigned entries, unsigned rows, unsigned kdim,
-                                          unsigned tile_rows) {
+                                          unsigned tile_rows, float join_us) {
   Line l;
   l.tiles = (rows + tile_rows - 1) / tile_rows;
   l.ksteps = (kdim + kK - 1) / kK;
-  l.total = entries * l.tiles * l.ksteps;
-  l.ctas = max(min(gridDim.x, l.total), 1u);
+  const unsigned units = entries * l.tiles;
+  l.total = units * l.ksteps;
+  const unsigned rounds = units / gridDim.x, rest = units - rounds * gridDim.x;
+  const float all = (float)(rounds * gridDim.x * l.ksteps) * 0.005f, k = (float)l.ksteps;
+  const float whole = fmaxf(all, (float)(rounds * l.ksteps) * 0.55f) +
+                      (rest ? fmaxf((float)rest * k * 0.005f, k * 0.55f) : 0.0f);
+  const float cut = fmaxf((float)l.total * 0.005f, (float)l.total / (float)gridDim.x * 0.55f);
+  l.quant = whole <= cut + join_us ? l.ksteps : 1u;
+  l.parts = l.total / l.quant;
+  l.ctas = max(min(gridDim.x, l.parts), 1u);
+  l.inv = 1.0 / (double)max(l.parts, 1u);
   return l;
 }
 
@@ -133,6 +165,20 @@ __device__ __forceinline__ bool wait_count(unsigned* p, unsigned n, ErrFlags* er
 }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Drain warps: whether `ok` holds in all of them.
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 
 // Drain warps: counts `v` after all of their earlier writes.
 __device__ __forceinline__ void epi_add(unsigned* p, unsigned v, int et) {
@@ -205,84 +251,128 @@ __device__ void token_choice(const MoeKArgs& a, int t, const double* logits) {
   }
 }
 
-// Logits: products of bf16 are exact in float32; 8 of them are added in float32 and the
-// sums in float64, so that close logits keep their order.
+// A token's logits by a cluster of CTAs that share its experts (one CTA alone reads a
+// router of 16 x 4096 in 10 us, most of it latency: with few tokens a cluster of 8 does).
+// Products of bf16 are exact in float32; 8 of them are added in float32 and the sums in
+// float64, so that close logits keep their order.  The grid is [tokens][cluster].
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const MoeKArgs a) {
-  __shared__ double logits[kMaxExperts];
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kW = kRouteThreads / 32;
+  __shared__ double logits[kMaxExperts];   // rank 0: of all experts
+  __shared__ double slices[kMaxExperts > kW ? kMaxExperts : kW];
+  const int t = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x, ranks = gridDim.x;
+  cluster_sync();   // every CTA of the cluster runs before one writes to another
   grid_dep_wait();
   grid_dep_launch();
-  if (t == 0) {
+  if (t == 0 && rank == 0) {
     unsigned* s = reinterpret_cast<unsigned*>(a.sync);
     for (unsigned i = threadIdx.x; i < sizeof(Sync) / 4; i += kRouteThreads) s[i] = 0u;
     if (threadIdx.x < sizeof(ErrFlags) / 4) reinterpret_cast<unsigned*>(a.err)[threadIdx.x] = 0u;
   }
+  // this CTA's experts rank, rank + ranks, ...; few of them are cut along D too
+  const int mine = (a.E - rank + ranks - 1) / ranks;
+  int cuts = 1;
+  while (mine * cuts * 2 <= kW) cuts *= 2;
   const int n8 = a.D / 8;
   const uint4* xr = reinterpret_cast<const uint4*>(a.x) + (int64_t)t * n8;
-  for (int e = warp; e < a.E; e += kRouteThreads / 32) {
+  for (int j = warp; j < mine * cuts; j += kW) {
+    const int e = rank + j / cuts * ranks, cut = j % cuts;
     const uint4* wr = reinterpret_cast<const uint4*>(a.wr) + (int64_t)e * n8;
     double acc = 0.0;
 #pragma unroll 8
-    for (int i = lane; i < n8; i += 32) {
+    for (int i = cut * 32 + lane; i < n8; i += 32 * cuts) {
       float xv[8], wv[8], s = 0.0f;
       unpack8(xr[i], xv);
       unpack8(__ldg(wr + i), wv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s = fmaf(xv[j], wv[j], s);
+      for (int q = 0; q < 8; ++q) s = fmaf(xv[q], wv[q], s);
       acc += (double)s;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) logits[e] = acc;
+    if (lane == 0) slices[j] = acc;
   }
   __syncthreads();
-  if (warp == 0) token_choice(a, t, logits);
+  const uint32_t to = leader_addr(smem_u32(logits));
+  for (int j = threadIdx.x; j < mine; j += kRouteThreads) {
+    double v = slices[j * cuts];
+    for (int c = 1; c < cuts; ++c) v += slices[j * cuts + c];
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to + (uint32_t)(rank + j * ranks) * 8u),
+                 "d"(v)
+                 : "memory");
+  }
+  cluster_sync();
+  if (rank == 0 && warp == 0) token_choice(a, t, logits);
 }
 
-// The lists of every CTA from the choices.
-__device__ void build_lists(const MoeKArgs& a, Lists& L) {
+// The lists of every CTA from the choices: a counting sort by expert.  `scratch` (the
+// ring, not in use yet): [chunks of 32 pairs][E] counts, then each pair's expert and its
+// place among its chunk's.
+__device__ void build_lists(const MoeKArgs& a, Lists& L, uint16_t* scratch) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int P = a.T * a.topk;
-  for (int e = tid; e < a.E; e += kThreads) L.count[e] = 0;
+  const int P = a.T * a.topk, chunks = (P + 31) / 32;
+  uint16_t* hist = scratch;
+  uint16_t* expert = hist + (chunks * a.E + 1) / 2 * 2;
+  uint16_t* place = expert + chunks * 32;
+  for (int i = tid; i < (chunks * a.E + 1) / 2; i += kThreads)
+    reinterpret_cast<uint32_t*>(hist)[i] = 0u;
   __syncthreads();
-  for (int p = tid; p < P; p += kThreads) {
-    const int e = a.idx[p];
-    L.ent[p] = (uint16_t)e;          // expert of the pair, until the blocks are known
-    atomicAdd(&L.count[e], 1);
+#pragma unroll 4
+  for (int c = warp; c < chunks; c += kWarps) {
+    const int p = c * 32 + lane;
+    const int e = p < P ? __ldcg(a.idx + p) : -1;
+    const unsigned m = __match_any_sync(0xffffffffu, e);
+    if (p < P) {
+      const int before = __popc(m & ((1u << lane) - 1u));
+      expert[p] = (uint16_t)e;
+      place[p] = (uint16_t)before;
+      if (before == 0) hist[c * a.E + e] = (uint16_t)__popc(m);
+    }
   }
   __syncthreads();
   for (int e = tid; e < a.E; e += kThreads) {
-    int first = 0, at = 0;
-    for (int q = 0; q < e; ++q) {
-      first += L.count[q];
-      at += (L.count[q] + a.NB - 1) / a.NB;
+    int n = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int q = hist[c * a.E + e];
+      hist[c * a.E + e] = (uint16_t)n;
+      n += q;
     }
-    const int n = L.count[e];
-    L.first[e] = first;
-    for (int r = 0; r < n; r += a.NB, ++at)
-      L.entry[at] = {(uint16_t)e, (uint16_t)(first + r), (uint16_t)min(a.NB, n - r), 0};
-    if (e == a.E - 1) L.n_entries = at;
+    L.count[e] = n;
   }
   __syncthreads();
-  // pairs of an expert in order of their token: a warp per expert in use
-  for (int e = warp; e < a.E; e += kWarps) {
-    if (L.count[e] == 0) continue;
-    int at = L.first[e];
-    for (int p0 = 0; p0 < P; p0 += 32) {
-      const int p = p0 + lane;
-      const bool hit = p < P && L.ent[p] == e;
-      const unsigned m = __ballot_sync(0xffffffffu, hit);
-      if (hit) {
-        const int r = at + __popc(m & ((1u << lane) - 1u));
-        L.token[r] = (uint16_t)(p / a.topk);
-        L.row[p] = (uint16_t)r;
+  if (warp == 0) {   // running sums of rows and of blocks over the experts
+    int rows = 0, blocks = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane, n = e < a.E ? L.count[e] : 0, nb = (n + a.NB - 1) / a.NB;
+      int r = n, b = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int r2 = __shfl_up_sync(0xffffffffu, r, o), b2 = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) {
+          r += r2;
+          b += b2;
+        }
       }
-      at += __popc(m);
+      if (e < a.E) {
+        L.first[e] = rows + r - n;
+        L.block[e] = (uint16_t)(blocks + b - nb);
+        for (int i = 0; i < nb; ++i)
+          L.entry[blocks + b - nb + i] = {(uint16_t)e, (uint16_t)(rows + r - n + i * a.NB),
+                                          (uint16_t)min(a.NB, n - i * a.NB), 0};
+      }
+      rows += __shfl_sync(0xffffffffu, r, 31);
+      blocks += __shfl_sync(0xffffffffu, b, 31);
     }
+    if (lane == 0) L.n_entries = blocks;
   }
   __syncthreads();
-  for (int i = warp; i < L.n_entries; i += kWarps)
-    for (int r = lane; r < L.entry[i].n; r += 32) L.ent[L.entry[i].r0 + r] = (uint16_t)i;
+  for (int p = tid; p < P; p += kThreads) {
+    const int e = expert[p], at = hist[(p >> 5) * a.E + e] + place[p], r = L.first[e] + at;
+    L.token[r] = (uint16_t)(p / a.topk);
+    L.ent[r] = (uint16_t)(L.block[e] + at / a.NB);
+    L.row[p] = (uint16_t)r;
+  }
+  fence_proxy_async_smem();   // TMA writes over the scratch
   __syncthreads();
 }
 
@@ -309,57 +399,97 @@ __device__ __forceinline__ float glu(float g, float u) { return act_apply(g, JM_
 // This CTA's share of a cut unit's h: partial tiles of CTAs c0..c1 in that order.
 __device__ void join_h(const MoeKArgs& a, const Entry& en, unsigned tile, unsigned c0, unsigned c1,
                        int et) {
-  const unsigned nseg = c1 - c0 + 1, total = en.n * 32u;
-  for (unsigned i = (blockIdx.x - c0) * 128 + et; i < total; i += nseg * 128) {
-    const unsigned r = i >> 5, f = (i & 31) * 4, col = tile * 128 + f;
-    if (col >= (unsigned)a.F) continue;
-    const float* p = part_of(a, 0, c0, 1) + r * 256 + f;
-    float4 g = ld4(p), u = ld4(p + 128);
-    for (unsigned c = c0 + 1; c <= c1; ++c) {
-      p = part_of(a, 0, c, 0) + r * 256 + f;
-      add4(g, ld4(p));
-      add4(u, ld4(p + 128));
+  constexpr int U = 2;   // items whose loads are in flight together
+  const unsigned nseg = c1 - c0 + 1, total = en.n * 32u, step = nseg * 128;
+  for (unsigned i0 = (blockIdx.x - c0) * 128 + et; i0 < total; i0 += U * step) {
+    float4 g[U], u[U];
+    int64_t at[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const unsigned i = min(i0 + q * step, total - 1);
+      at[q] = (int64_t)(i >> 5) * 256 + (i & 31) * 4;
+      const float* p = part_of(a, 0, c0, 1) + at[q];
+      g[q] = ld4(p);
+      u[q] = ld4(p + 128);
     }
-    *reinterpret_cast<uint2*>(a.h + (int64_t)(en.r0 + r) * a.F + col) =
-        make_uint2(pack2(glu(g.x, u.x), glu(g.y, u.y)), pack2(glu(g.z, u.z), glu(g.w, u.w)));
+#pragma unroll 2
+    for (unsigned c = c0 + 1; c <= c1; ++c) {
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const float* p = part_of(a, 0, c, 0) + at[q];
+        add4(g[q], ld4(p));
+        add4(u[q], ld4(p + 128));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const unsigned i = i0 + q * step, col = tile * 128 + (i & 31) * 4;
+      if (i < total && col < (unsigned)a.F)
+        *reinterpret_cast<uint2*>(a.h + (int64_t)(en.r0 + (i >> 5)) * a.F + col) =
+            make_uint2(pack2(glu(g[q].x, u[q].x), glu(g[q].y, u[q].y)),
+                       pack2(glu(g[q].z, u[q].z), glu(g[q].w, u[q].w)));
+    }
   }
 }
 
-// out of every token: its experts' products weighted in the order of the choices.
-__device__ void form_out(const MoeKArgs& a, const Lists& L, const Line& l, int et) {
-  const unsigned d4 = (unsigned)a.D / 4, total = (unsigned)a.T * d4;
+// out of every token: its experts' products weighted in the order of the choices.  A
+// thread takes U groups of 4 columns at a time, so that their loads are in flight together.
+template <int U>
+__device__ __forceinline__ void form_out(const MoeKArgs& a, const Lists& L, const Line& l) {
+  const unsigned d4 = (unsigned)a.D / 4, total = (unsigned)a.T * d4, step = gridDim.x * kThreads;
   const int64_t width = (int64_t)l.tiles * 256;
-  for (unsigned i = blockIdx.x * 128 + et; i < total; i += gridDim.x * 128) {
-    const unsigned t = i / d4, d = (i - t * d4) * 4, tile = d >> 8, in = d & 255;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (unsigned i0 = blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += U * step) {
+    float4 o[U];
+    uint2 res[U];
+    unsigned t[U], d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const unsigned i = min(i0 + u * step, total - 1);
+      t[u] = i / d4;
+      d[u] = (i - t[u] * d4) * 4;
+      res[u] = make_uint2(0u, 0u);
+      if (a.residual) res[u] = reinterpret_cast<const uint2*>(a.residual)[i];
+    }
     for (int c = 0; c < a.topk; ++c) {
-      const unsigned p = t * a.topk + c;
-      const int r = L.row[p], ent = L.ent[r];
-      const float w = a.wgt[p];
-      const unsigned s0 = (ent * l.tiles + tile) * l.ksteps;
-      const unsigned c0 = l.cta_of(s0), c1 = l.cta_of(s0 + l.ksteps - 1);
-      float4 v;
-      if (c0 == c1) {
-        v = ld4(a.y + r * width + d);
-      } else {
-        const int64_t at = (int64_t)(r - L.entry[ent].r0) * 256 + in;
-        v = ld4(part_of(a, 1, c0, 1) + at);
-        for (unsigned q = c0 + 1; q <= c1; ++q) add4(v, ld4(part_of(a, 1, q, 0) + at));
+      float4 v[U];
+      float w[U];
+      const float* next[U];
+      unsigned more[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const unsigned p = t[u] * a.topk + c;
+        const int r = L.row[p], ent = L.ent[r];
+        w[u] = a.wgt[p];
+        unsigned c0, c1;
+        l.ctas_of(ent * l.tiles + (d[u] >> 8), c0, c1);
+        const int64_t at = (int64_t)(r - L.entry[ent].r0) * 256 + (d[u] & 255);
+        v[u] = ld4(c0 == c1 ? a.y + r * width + d[u] : part_of(a, 1, c0, 1) + at);
+        next[u] = part_of(a, 1, c0 + 1, 0) + at;
+        more[u] = c1 - c0;
       }
-      o.x = fmaf(w, v.x, o.x);
-      o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z);
-      o.w = fmaf(w, v.w, o.w);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* q = next[u];
+#pragma unroll 8
+        for (unsigned k = 0; k < more[u]; ++k) add4(v[u], ld4(q + (int64_t)k * a.NB * 512));
+        o[u].x = fmaf(w[u], v[u].x, o[u].x);
+        o[u].y = fmaf(w[u], v[u].y, o[u].y);
+        o[u].z = fmaf(w[u], v[u].z, o[u].z);
+        o[u].w = fmaf(w[u], v[u].w, o[u].w);
+      }
     }
-    const int64_t at = (int64_t)t * a.D + d;
-    if (a.residual) {
-      const uint2 q = *reinterpret_cast<const uint2*>(a.residual + at);
-      o.x += __uint_as_float(q.x << 16);
-      o.y += __uint_as_float(q.x & 0xffff0000u);
-      o.z += __uint_as_float(q.y << 16);
-      o.w += __uint_as_float(q.y & 0xffff0000u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned i = i0 + u * step;
+      if (i >= total) break;
+      const uint2 q = res[u];
+      reinterpret_cast<uint2*>(a.out)[i] =
+          make_uint2(pack2(o[u].x + __uint_as_float(q.x << 16),
+                           o[u].y + __uint_as_float(q.x & 0xffff0000u)),
+                     pack2(o[u].z + __uint_as_float(q.y << 16),
+                           o[u].w + __uint_as_float(q.y & 0xffff0000u)));
     }
-    *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
   }
 }
 
@@ -378,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int epi_flag;
   Lists& L = *reinterpret_cast<Lists*>(smem + S * stage_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t tmem_cols = 4 * a.NB;   // two accumulators of two row groups: 64..512
+  uint32_t tmem_cols = 64;   // two accumulators of two row groups
+  while (tmem_cols < 4u * a.NB) tmem_cols *= 2;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -401,12 +532,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   grid_dep_wait();
-  build_lists(a, L);
+  build_lists(a, L, reinterpret_cast<uint16_t*>(smem));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const Line line[2] = {make_line(L.n_entries, a.F, a.D, 128), make_line(L.n_entries, a.D, a.F, 256)};
+  // (partial tiles cost the first phase a round of counting and of h, 5 us; the second
+  // sums them where it has to wait anyway)
+  const Line line[2] = {make_line(L.n_entries, a.F, a.D, 128, 5.0f),
+                        make_line(L.n_entries, a.D, a.F, 256, 1.0f)};
 
   if (warp == 0) {
     if (lane == 0) {
@@ -576,41 +710,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&acc_empty[b]));
-        if (ph == 0) {
-          if (whole) {
-            fence_proxy_async_global();   // h is read by TMA
-            epi_add(&a.sync->ready[ent], l.ksteps, et);
-          } else {
-            epi_add(&a.sync->unit[l.cta_of(u0)], end - s, et);
-          }
-        }
         s = end;
       }
       if (ph == 0) {
-        // this CTA's share of the cut units it took part in (its first and its last),
-        // after all that others wait for is stored
+        // What others wait for is counted once, behind one fence: a fence after each unit
+        // held the drain up for 2 us of every 4 with units of 3 steps.
+        fence_proxy_async_global();   // h is read by TMA
+        __threadfence();
+        ok = epi_all(ok);
         for (unsigned s = s0; ok && s < s1;) {
           const unsigned u = s / l.ksteps, u0 = u * l.ksteps, end = min(s1, u0 + l.ksteps);
-          const unsigned ent = u / l.tiles;
-          if (s != u0 || end != u0 + l.ksteps) {
-            const unsigned c0 = l.cta_of(u0), c1 = l.cta_of(u0 + l.ksteps - 1);
-            ok = epi_wait(&a.sync->unit[c0], l.ksteps, a.err, 98, et, &epi_flag);
-            if (ok) {
-              join_h(a, L.entry[ent], u - ent * l.tiles, c0, c1, et);
-              fence_proxy_async_global();
-              epi_add(&a.sync->ready[ent], end - s, et);
+          if (et == 0) {
+            if (s == u0 && end == u0 + l.ksteps) {
+              // all whole units of the block at once
+              const unsigned block_end = (u / l.tiles + 1) * l.tiles * l.ksteps;
+              const unsigned stop = min(s1 / l.ksteps * l.ksteps, block_end);
+              add_release(&a.sync->ready[u / l.tiles], stop - s);
+              s = stop;
+              continue;
             }
+            unsigned c0, c1;
+            l.ctas_of(u, c0, c1);
+            add_release(&a.sync->unit[c0], end - s);
           }
           s = end;
+        }
+        // This CTA's share of the cut units it took part in: its first and its last.
+        unsigned cut_u[2], cut_steps[2];
+        int cuts = 0;
+        for (unsigned s = s0; s < s1 && cuts < 2;) {
+          const unsigned u = s / l.ksteps, u0 = u * l.ksteps, end = min(s1, u0 + l.ksteps);
+          if (s != u0 || end != u0 + l.ksteps) {
+            cut_u[cuts] = u;
+            cut_steps[cuts++] = end - s;
+            s = end;
+          } else {   // past the whole units
+            s = s1 / l.ksteps * l.ksteps;
+          }
+        }
+        for (int i = 0; ok && i < cuts; ++i) {
+          unsigned c0, c1;
+          l.ctas_of(cut_u[i], c0, c1);
+          ok = epi_wait(&a.sync->unit[c0], l.ksteps, a.err, 98, et, &epi_flag);
+          const unsigned ent = cut_u[i] / l.tiles;
+          if (ok) join_h(a, L.entry[ent], cut_u[i] - ent * l.tiles, c0, c1, et);
+        }
+        if (ok && cuts) {
+          fence_proxy_async_global();
+          __threadfence();
+          epi_sync();
+          for (int i = 0; et == 0 && i < cuts; ++i)
+            add_release(&a.sync->ready[cut_u[i] / l.tiles], cut_steps[i]);
         }
       }
     }
     epi_add(&a.sync->done, 1, et);
-    if (epi_wait(&a.sync->done, gridDim.x, a.err, 99, et, &epi_flag))
-      form_out(a, L, line[1], et);
+    epi_wait(&a.sync->done, gridDim.x, a.err, 99, et, &epi_flag);
   }
   tc_fence_before();
   __syncthreads();
+  if (epi_flag) {
+    if ((unsigned)a.T * a.D / 4 <= gridDim.x * kThreads)
+      form_out<1>(a, L, line[1]);
+    else
+      form_out<4>(a, L, line[1]);
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, tmem_cols);
@@ -652,9 +816,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int moe_block(int64_t T, int64_t E, int64_t k) {
   int64_t want = 2 * ceil_div(T * k, E) + 16;
   if (want > T) want = T;
-  int nb = 16;
-  while (nb < want && nb < kMaxBlock) nb *= 2;
-  return nb;
+  const int nb = (int)ceil_div(want, 16) * 16;
+  return nb < 16 ? 16 : nb < kMaxBlock ? nb : kMaxBlock;
 }
 
 constexpr size_t kSmemMost = 227 * 1024;
@@ -765,20 +928,25 @@ cudaError_t run_moe(const MoeArgs& m, Problem& p) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeCooperative;
-  attr[1].val.cooperative = 1;
+  // CTAs a token's experts are shared by: up to 8, while the grid stays below two waves
+  int ranks = 8;
+  while (ranks > 1 && (ranks > m.E || m.T * ranks > 2 * ctas)) ranks /= 2;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 2;
   cfg.stream = p.stream;
-  cfg.gridDim = dim3((unsigned)m.T);
+  cfg.gridDim = dim3((unsigned)ranks, (unsigned)m.T);
   cfg.blockDim = dim3(kRouteThreads);
-  cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, k_moe_route, a);
   if (e != cudaSuccess) return e;
   launched(p, "k_moe_route");
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = ring_smem(a.NB);
-  cfg.attrs = attr + 1;
   e = cudaLaunchKernelEx(&cfg, k_moe, wg, wu, wd, tx, th, a);
   if (e == cudaSuccess) launched(p, "k_moe");
   return e;

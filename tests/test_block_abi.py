@@ -222,3 +222,10 @@ def test_moe_rejects_bad_pointers():
     assert moe_fwd(d, nbytes=n - 1) == jmix.JM_ERR_WORKSPACE
     assert moe_fwd(d, workspace=None) == jmix.JM_ERR_WORKSPACE
     assert moe_fwd(d, workspace=W + 64) == jmix.JM_ERR_WORKSPACE
+
+
+def test_moe_workspace_size_of_every_token_count():
+    for t in range(257):
+        for e, k in ((1, 1), (16, 2), (256, 8)):
+            n = jmix.jm_moe_fwd_workspace_size(jmix.moe_dims(t, 64, 128, e, k))
+            assert n >= 256 and n % 256 == 0
