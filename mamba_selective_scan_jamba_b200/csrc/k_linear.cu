@@ -49,7 +49,7 @@ constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 
 
 struct PairArgs {
   int64_t M, N, K;
-  int64_t m_tiles, n_tiles;
+  unsigned m_tiles, n_tiles;
   int splits;    // above 1: float32 partial tiles [splits][M][N] through tm_out
   Epilogue ep;   // (its out and residual are reached through the maps)
   ErrFlags* err;
@@ -80,25 +80,43 @@ __device__ __forceinline__ void apply_act(uint32_t (&v)[64], int act) {
 }
 
 struct Item {
-  int64_t mt, nt;
+  unsigned mt, nt, split;
   int k0, k1;    // K chunks [k0, k1)
-  int split;
 };
 
-__device__ __forceinline__ Item item_of(const PairArgs& g, int64_t w, int kchunks) {
+// (32-bit throughout: a 64-bit division is several hundred cycles of one thread)
+__device__ __forceinline__ Item item_of(const PairArgs& g, unsigned w, int kchunks) {
   Item it;
-  const int64_t tiles = g.m_tiles * g.n_tiles;
-  it.split = (int)(w / tiles);
-  const int64_t t = w - (int64_t)it.split * tiles;
-  const int64_t per_group = (int64_t)kGroupM * g.n_tiles;
-  const int64_t grp = t / per_group, idx = t - grp * per_group;
-  const int64_t rows = min((int64_t)kGroupM, g.m_tiles - grp * kGroupM);
-  it.mt = grp * kGroupM + idx % rows;
+  const unsigned tiles = g.m_tiles * g.n_tiles;
+  it.split = g.splits > 1 ? w / tiles : 0u;
+  const unsigned t = w - it.split * tiles;
+  const unsigned per_group = (unsigned)kGroupM * g.n_tiles;
+  const unsigned grp = t / per_group, idx = t - grp * per_group;
+  const unsigned rows = min((unsigned)kGroupM, g.m_tiles - grp * kGroupM);
   it.nt = idx / rows;
-  it.k0 = (int)((int64_t)kchunks * it.split / g.splits);
-  it.k1 = (int)((int64_t)kchunks * (it.split + 1) / g.splits);
+  it.mt = grp * kGroupM + idx - it.nt * rows;
+  it.k0 = 0;
+  it.k1 = kchunks;
+  if (g.splits > 1) {
+    it.k0 = (int)((int64_t)kchunks * it.split / g.splits);
+    it.k1 = (int)((int64_t)kchunks * (it.split + 1) / g.splits);
+  }
   return it;
 }
+
+// A place in the ring and the parity of its round: counted on, since a division by the
+// number of stages in each step of one thread's loop is time that the loads do not have.
+template <int S>
+struct Place {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == S) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 template <bool AMN, bool BMN, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -121,8 +139,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
-  const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int64_t items = g.m_tiles * g.n_tiles * g.splits;
+  const unsigned pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const unsigned items = g.m_tiles * g.n_tiles * g.splits;
   const int kchunks = (int)((g.K + kK - 1) / kK);
 
   if (threadIdx.x == 0) {
@@ -158,21 +176,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int64_t it = 0;
+      Place<S> at;
       bool ok = true;
-      for (int64_t w = pair; ok && w < items; w += npairs) {
+      const uint32_t fb0 = leader_addr(smem_u32(full)), base = smem_u32(smem);
+      for (unsigned w = pair; ok && w < items; w += npairs) {
         const Item q = item_of(g, w, kchunks);
         const int32_t m0 = (int32_t)(q.mt * (2 * kHalf) + rank * kHalf);
         const int32_t n0 = (int32_t)(q.nt * BN + rank * kBHalf);
-        for (int kc = q.k0; kc < q.k1; ++kc, ++it) {
-          const int s = (int)(it % S);
-          if (it >= S &&
-              !mbar_wait(smem_u32(&empty[s]), (uint32_t)((it / S) - 1) & 1u, g.err, 81)) {
+        for (int kc = q.k0; kc < q.k1; ++kc, at.next()) {
+          const int s = at.s;   // (the first round's wait for "empty" returns at once)
+          if (!mbar_wait(smem_u32(&empty[s]), at.parity ^ 1u, g.err, 81)) {
             ok = false;
             break;
           }
-          const uint32_t st = smem_u32(smem + s * kStage);
-          const uint32_t fb = leader_addr(smem_u32(&full[s]));
+          const uint32_t st = base + (uint32_t)(s * kStage), fb = fb0 + (uint32_t)(s * 8);
           // the leader expects both CTAs' bytes on its barrier
           if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), (uint32_t)(2 * kStage));
           if constexpr (AMN) {   // boxes of 64 m values x 64 k rows
@@ -194,23 +211,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       const uint32_t idesc = idesc_bf16_f32_major(2 * kHalf, BN, AMN, BMN);
-      int64_t it = 0, j = 0;
+      Place<S> at;
+      Place<2> acc;
       bool ok = true;
-      for (int64_t w = pair; ok && w < items; w += npairs, ++j) {
+      const uint32_t base = smem_u32(smem);
+      for (unsigned w = pair; ok && w < items; w += npairs, acc.next()) {
         const Item q = item_of(g, w, kchunks);
-        const int b = (int)(j & 1);
-        if (j >= 2 && !mbar_wait(smem_u32(&acc_empty[b]), (uint32_t)((j >> 1) - 1) & 1u, g.err, 82))
-          break;
+        const int b = acc.s;
+        if (!mbar_wait(smem_u32(&acc_empty[b]), acc.parity ^ 1u, g.err, 82)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + (uint32_t)(b * 256);
-        for (int kc = q.k0; kc < q.k1; ++kc, ++it) {
-          const int s = (int)(it % S);
-          if (!mbar_wait(smem_u32(&full[s]), (uint32_t)(it / S) & 1u, g.err, 83)) {
+        for (int kc = q.k0; kc < q.k1; ++kc, at.next()) {
+          const int s = at.s;
+          if (!mbar_wait(smem_u32(&full[s]), at.parity, g.err, 83)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ab = smem_u32(smem + s * kStage), bb = ab + kABytes;
+          const uint32_t ab = base + (uint32_t)(s * kStage), bb = ab + kABytes;
 #pragma unroll
           for (int kk = 0; kk < kK / 16; ++kk) {
             const uint64_t ad = AMN ? sw128_mnmajor_desc(ab + kk * 2048, 8192)
@@ -237,14 +255,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int sw = r & 7;                             // the swizzle of this row
     const uint32_t res_bar = smem_u32(&res_full[grp]);
     uint32_t res_phase = 0;
-    int64_t j = 0;
+    Place<2> acc;
     // (a thread whose wait ran out goes on without waiting, so that its group's barriers
     // stay matched; the error header says that the values are not to be used)
     bool ok = true;
-    for (int64_t w = pair; w < items; w += npairs, ++j) {
+    for (unsigned w = pair; w < items; w += npairs, acc.next()) {
       const Item q = item_of(g, w, kchunks);
-      const int b = (int)(j & 1);
-      const int64_t row0 = q.mt * (2 * kHalf) + rank * kHalf, n0 = q.nt * BN;
+      const int b = acc.s;
+      const int64_t row0 = (int64_t)q.mt * (2 * kHalf) + rank * kHalf, n0 = (int64_t)q.nt * BN;
       const bool rows = row0 < g.M;
       const uint32_t tbase = tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(b * 256);
       bool waited = false;
@@ -258,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         group_sync(grp);
-        if (!waited) ok = ok && mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(j >> 1) & 1u, g.err, 84);
+        if (!waited) ok = ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
         waited = true;
         tc_fence_after();
         uint32_t v[64];
@@ -325,14 +343,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         group_sync(grp);
         if (first) {
           if (split)
-            tma_store_3d(&tm_out, smem_u32(stage), (int32_t)col, (int32_t)row0, q.split);
+            tma_store_3d(&tm_out, smem_u32(stage), (int32_t)col, (int32_t)row0, (int32_t)q.split);
           else
             tma_store_2d(&tm_out, smem_u32(stage), (int32_t)col, (int32_t)row0);
           bulk_commit();
         }
       }
       // the accumulator is free once it is complete and this warp has read its part
-      if (!waited) ok = ok && mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(j >> 1) & 1u, g.err, 84);
+      if (!waited) ok = ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty_leader + (uint32_t)(b * 8));
@@ -536,7 +554,7 @@ cudaError_t launch_pair(const CUtensorMap (&tm)[5], const PairArgs& g, cudaStrea
   if (e != cudaSuccess) return e;
   const int most = cached_attr(cache, dev, query_pairs<AMN, BMN, BN>);
   if (most <= 0) return cudaErrorInvalidConfiguration;
-  const int64_t items = g.m_tiles * g.n_tiles * g.splits;
+  const int64_t items = (int64_t)g.m_tiles * g.n_tiles * g.splits;
   const int64_t pairs = items < most ? items : most;
   return launch(k_linear_pair<AMN, BMN, BN>, dim3((unsigned)(2 * pairs)), dim3(kThreads),
                 (size_t)smem_bytes(BN), s, tm[0], tm[1], tm[2], tm[3], tm[4], g);
@@ -560,8 +578,8 @@ cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* 
   g.M = M;
   g.N = N;
   g.K = K;
-  g.m_tiles = (M + 255) / 256;
-  g.n_tiles = (N + c.bn - 1) / c.bn;
+  g.m_tiles = (unsigned)((M + 255) / 256);
+  g.n_tiles = (unsigned)((N + c.bn - 1) / c.bn);
   g.splits = c.splits;
   g.ep = ep;
   g.err = err;

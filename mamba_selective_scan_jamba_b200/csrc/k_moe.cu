@@ -146,6 +146,43 @@ __device__ __forceinline__ Line make_line(unsigned entries, unsigned rows, unsig
   return l;
 }
 
+// A CTA's walk over its range of a line, unit by unit (divisions only at its start: with
+// one or two in each step of the producing thread a step took it 550 ns).
+struct Walk {
+  unsigned s, s1, ent, tile, k, ksteps, tiles;
+  __device__ __forceinline__ Walk(const Line& l) : ksteps(l.ksteps), tiles(l.tiles) {
+    s = l.start(blockIdx.x);
+    s1 = l.start(blockIdx.x + 1);
+    const unsigned u = s / ksteps;
+    k = s - u * ksteps;
+    ent = u / tiles;
+    tile = u - ent * tiles;
+  }
+  __device__ __forceinline__ bool more() const { return s < s1; }
+  // steps of the present unit in the range
+  __device__ __forceinline__ unsigned steps() const { return min(s1 - s, ksteps - k); }
+  __device__ __forceinline__ bool whole() const { return k == 0 && s1 - s >= ksteps; }
+  __device__ __forceinline__ void next() {
+    s += steps();
+    k = 0;
+    if (++tile == tiles) {
+      tile = 0;
+      ++ent;
+    }
+  }
+};
+
+// A place in a ring of n and the parity of its round.
+struct Place {
+  unsigned s = 0, parity = 0;
+  __device__ __forceinline__ void next(unsigned n) {
+    if (++s == n) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
 // ------------------------------------------------------ counters between CTAs
 __device__ __forceinline__ void add_release(unsigned* p, unsigned v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
@@ -545,139 +582,133 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = l2_evict_first_policy();   // weights pass through once
-      unsigned it = 0;
+      const uint32_t base = smem_u32(smem);
+      Place at;
       bool ok = true;
       for (int ph = 0; ok && ph < 2; ++ph) {
-        const Line& l = line[ph];
-        const unsigned s1 = l.start(blockIdx.x + 1);
-        for (unsigned s = l.start(blockIdx.x); s < s1; ++s, ++it) {
-          const unsigned u = s / l.ksteps, ent = u / l.tiles;
-          const int k = (int)(s - u * l.ksteps) * kK, tile = (int)(u - ent * l.tiles);
-          const int e = L.entry[ent].e;
-          const unsigned st = it % S;
-          if (it >= (unsigned)S &&
-              !mbar_wait(smem_u32(&empty[st]), ((it / S) - 1) & 1u, a.err, 92)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = smem_u32(&full[st]), dst = smem_u32(smem + st * stage_bytes);
-          mbar_arrive_expect_tx(fb, kWBytes);
-          if (ph == 0) {
-            tma_load_3d(dst, &tm_wg, fb, k, tile * 128, e, pol);
-            tma_load_3d(dst + kSlabBytes, &tm_wu, fb, k, tile * 128, e, pol);
-          } else {
-            tma_load_3d(dst, &tm_wd, fb, k, tile * 256, e, pol);
-            tma_load_3d(dst + kSlabBytes, &tm_wd, fb, k, tile * 256 + 128, e, pol);
+        for (Walk w(line[ph]); ok && w.more(); w.next()) {
+          const int e = L.entry[w.ent].e, row = (int)w.tile * (ph == 0 ? 128 : 256);
+          int k = (int)w.k * kK;
+          for (unsigned n = w.steps(); n > 0; --n, k += kK, at.next(S)) {
+            // (the first round's wait for "empty" returns at once)
+            if (!mbar_wait(smem_u32(&empty[at.s]), at.parity ^ 1u, a.err, 92)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb = smem_u32(&full[at.s]), dst = base + at.s * stage_bytes;
+            mbar_arrive_expect_tx(fb, kWBytes);
+            if (ph == 0) {
+              tma_load_3d(dst, &tm_wg, fb, k, row, e, pol);
+              tma_load_3d(dst + kSlabBytes, &tm_wu, fb, k, row, e, pol);
+            } else {
+              tma_load_3d(dst, &tm_wd, fb, k, row, e, pol);
+              tma_load_3d(dst + kSlabBytes, &tm_wd, fb, k, row + 128, e, pol);
+            }
           }
         }
       }
     }
   } else if (warp == 6) {
-    unsigned it = 0;
+    const uint32_t base = smem_u32(smem) + kWBytes;
+    Place at;
     bool ok = true;
     for (int ph = 0; ok && ph < 2; ++ph) {
-      const Line& l = line[ph];
-      const unsigned s1 = l.start(blockIdx.x + 1);
-      unsigned ready = ~0u;   // the block whose h is known to be there
-      for (unsigned s = l.start(blockIdx.x); s < s1; ++s, ++it) {
-        const unsigned u = s / l.ksteps, ent = u / l.tiles;
-        const int k = (int)(s - u * l.ksteps) * kK;
-        const Entry en = L.entry[ent];
+      unsigned have = ~0u;   // the block whose h is known to be there, or whose rows are held
+      int t[4] = {};         // rows 4 lane .. 4 lane + 3 of the block
+      for (Walk w(line[ph]); ok && w.more(); w.next()) {
+        const Entry en = L.entry[w.ent];
         const int n16 = (en.n + 15) / 16;
-        const unsigned st = it % S;
-        int w = 1;
-        if (lane == 0) {
-          if (ph == 1 && ent != ready)
-            w = wait_count(&a.sync->ready[ent], line[0].tiles * line[0].ksteps, a.err, 93) ? 1 : 0;
-          if (w && it >= (unsigned)S)
-            w = mbar_wait(smem_u32(&empty[st]), ((it / S) - 1) & 1u, a.err, 94) ? 1 : 0;
-        }
-        if (__shfl_sync(0xffffffffu, w, 0) == 0) {
-          ok = false;
-          break;
-        }
-        __syncwarp();
-        if (ph == 1 && ent != ready) {
-          fence_proxy_async_global();
-          ready = ent;
-        }
-        const uint32_t fb = smem_u32(&full[st]);
-        const uint32_t dst = smem_u32(smem + st * stage_bytes + kWBytes);
-        if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(n16 * 16 * 128));
-        __syncwarp();
-        if (ph == 0) {
-          // 4 rows by index at a time; rows behind the last repeat it (their columns of
-          // the accumulator are not read)
-          for (int r = lane * 4; r < n16 * 16; r += 128) {
-            int t[4];
+        if (w.ent != have) {
+          have = w.ent;
+          if (ph == 0) {
+            // rows behind the last repeat it (their columns of the accumulator are not read)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) t[j] = L.token[en.r0 + min(r + j, en.n - 1)];
-            tma_gather4(dst + r * 128, &tm_x, fb, k, t[0], t[1], t[2], t[3]);
+            for (int j = 0; j < 4; ++j) t[j] = L.token[en.r0 + min(lane * 4 + j, en.n - 1)];
+          } else {
+            int there = 1;
+            if (lane == 0)
+              there = wait_count(&a.sync->ready[w.ent], line[0].tiles * line[0].ksteps, a.err, 93);
+            if (__shfl_sync(0xffffffffu, there, 0) == 0) {
+              ok = false;
+              break;
+            }
+            fence_proxy_async_global();
           }
-        } else if (lane < n16) {
-          tma_load_2d(dst + lane * 2048, &tm_h, fb, k, en.r0 + lane * 16);
+        }
+        int k = (int)w.k * kK;
+        for (unsigned n = w.steps(); n > 0; --n, k += kK, at.next(S)) {
+          // (every lane waits: each of them may issue a load into the stage)
+          ok = mbar_wait(smem_u32(&empty[at.s]), at.parity ^ 1u, a.err, 94);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(&full[at.s]), dst = base + at.s * stage_bytes;
+          if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(n16 * 16 * 128));
+          __syncwarp();
+          if (ph == 0) {
+            // 4 rows by index at a time: 16 rows of a block by 4 lanes
+            if (lane < n16 * 4) tma_gather4(dst + lane * 512, &tm_x, fb, k, t[0], t[1], t[2], t[3]);
+          } else if (lane < n16) {
+            tma_load_2d(dst + lane * 2048, &tm_h, fb, k, en.r0 + lane * 16);
+          }
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      unsigned it = 0, j = 0;
+      const uint32_t base = smem_u32(smem);
+      Place at, acc;
       bool ok = true;
       for (int ph = 0; ok && ph < 2; ++ph) {
-        const Line& l = line[ph];
-        const unsigned s1 = l.start(blockIdx.x + 1);
-        for (unsigned s = l.start(blockIdx.x); ok && s < s1; ++j) {
-          const unsigned u = s / l.ksteps, end = min(s1, (u + 1) * l.ksteps);
-          const int n16 = (L.entry[u / l.tiles].n + 15) / 16;
+        for (Walk w(line[ph]); ok && w.more(); w.next(), acc.next(2)) {
+          const int n16 = (L.entry[w.ent].n + 15) / 16;
           const uint32_t idesc = idesc_bf16_f32(128, n16 * 16);
-          const unsigned b = j & 1;
-          if (j >= 2 && !mbar_wait(smem_u32(&acc_empty[b]), ((j >> 1) - 1) & 1u, a.err, 95)) {
+          if (!mbar_wait(smem_u32(&acc_empty[acc.s]), acc.parity ^ 1u, a.err, 95)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem + b * (uint32_t)(2 * a.NB);
-          for (const unsigned first = s; s < end; ++s, ++it) {
-            const unsigned st = it % S;
-            if (!mbar_wait(smem_u32(&full[st]), (it / S) & 1u, a.err, 96)) {
+          const uint32_t d = tmem + acc.s * (uint32_t)(2 * a.NB);
+          uint32_t add = 0u;
+          for (unsigned n = w.steps(); n > 0; --n, at.next(S)) {
+            if (!mbar_wait(smem_u32(&full[at.s]), at.parity, a.err, 96)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t wa = smem_u32(smem + st * stage_bytes), xb = wa + kWBytes;
+            const uint32_t wa = base + at.s * stage_bytes, xb = wa + kWBytes;
 #pragma unroll
             for (int g = 0; g < 2; ++g)
 #pragma unroll
               for (int kk = 0; kk < kK / 16; ++kk)
                 umma_f16(d + (uint32_t)(g * a.NB),
                          sw128_kmajor_desc(wa + g * kSlabBytes + kk * 32),
-                         sw128_kmajor_desc(xb + kk * 32), idesc, (s > first || kk > 0) ? 1u : 0u);
-            umma_commit(smem_u32(&empty[st]));
+                         sw128_kmajor_desc(xb + kk * 32), idesc, kk > 0 ? 1u : add);
+            add = 1u;
+            umma_commit(smem_u32(&empty[at.s]));
           }
-          if (ok) umma_commit(smem_u32(&acc_full[b]));
+          if (ok) umma_commit(smem_u32(&acc_full[acc.s]));
         }
       }
     }
   } else {
     const int lg = warp & 3, et = lg * 32 + lane;   // TMEM lane = weight row of a group
-    unsigned j = 0;
+    Place acc;
     bool ok = true;
     for (int ph = 0; ok && ph < 2; ++ph) {
       const Line& l = line[ph];
-      const unsigned s0 = l.start(blockIdx.x), s1 = l.start(blockIdx.x + 1);
-      for (unsigned s = s0; s < s1; ++j) {
-        const unsigned u = s / l.ksteps, u0 = u * l.ksteps, end = min(s1, u0 + l.ksteps);
-        const unsigned ent = u / l.tiles, tile = u - ent * l.tiles;
-        const bool whole = s == u0 && end == u0 + l.ksteps;
+      for (Walk w(l); w.more(); w.next(), acc.next(2)) {
+        const unsigned ent = w.ent, tile = w.tile, b = acc.s;
+        const bool whole = w.whole();
         const Entry en = L.entry[ent];
-        const unsigned b = j & 1;
-        if (!mbar_wait(smem_u32(&acc_full[b]), (j >> 1) & 1u, a.err, 97)) {
+        if (!mbar_wait(smem_u32(&acc_full[b]), acc.parity, a.err, 97)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t tb = tmem + ((uint32_t)(lg * 32) << 16) + b * (uint32_t)(2 * a.NB);
-        float* dst = part_of(a, ph, blockIdx.x, s == u0 ? 1 : 0) + et;
+        float* dst = part_of(a, ph, blockIdx.x, w.k == 0 ? 1 : 0) + et;
         int64_t pitch = 256;
         if (ph == 1 && whole) {
           pitch = (int64_t)l.tiles * 256;
@@ -710,7 +741,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&acc_empty[b]));
-        s = end;
       }
       if (ph == 0) {
         // What others wait for is counted once, behind one fence: a fence after each unit
@@ -718,36 +748,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_global();   // h is read by TMA
         __threadfence();
         ok = epi_all(ok);
-        for (unsigned s = s0; ok && s < s1;) {
-          const unsigned u = s / l.ksteps, u0 = u * l.ksteps, end = min(s1, u0 + l.ksteps);
-          if (et == 0) {
-            if (s == u0 && end == u0 + l.ksteps) {
-              // all whole units of the block at once
-              const unsigned block_end = (u / l.tiles + 1) * l.tiles * l.ksteps;
-              const unsigned stop = min(s1 / l.ksteps * l.ksteps, block_end);
-              add_release(&a.sync->ready[u / l.tiles], stop - s);
-              s = stop;
-              continue;
+        // The cut units this CTA took part in are its first and its last.
+        unsigned cut_u[2], cut_steps[2], block = ~0u, done = 0;
+        int cuts = 0;
+        for (Walk w(l); ok && w.more(); w.next()) {
+          const unsigned u = w.ent * w.tiles + w.tile;
+          if (w.whole()) {   // counted for all units of a block at once
+            if (w.ent != block && done) {
+              if (et == 0) add_release(&a.sync->ready[block], done);
+              done = 0;
             }
+            block = w.ent;
+            done += w.ksteps;
+          } else {
             unsigned c0, c1;
             l.ctas_of(u, c0, c1);
-            add_release(&a.sync->unit[c0], end - s);
-          }
-          s = end;
-        }
-        // This CTA's share of the cut units it took part in: its first and its last.
-        unsigned cut_u[2], cut_steps[2];
-        int cuts = 0;
-        for (unsigned s = s0; s < s1 && cuts < 2;) {
-          const unsigned u = s / l.ksteps, u0 = u * l.ksteps, end = min(s1, u0 + l.ksteps);
-          if (s != u0 || end != u0 + l.ksteps) {
             cut_u[cuts] = u;
-            cut_steps[cuts++] = end - s;
-            s = end;
-          } else {   // past the whole units
-            s = s1 / l.ksteps * l.ksteps;
+            cut_steps[cuts++] = w.steps();
+            if (et == 0) add_release(&a.sync->unit[c0], w.steps());
           }
         }
+        if (done && et == 0) add_release(&a.sync->ready[block], done);
+        // Its share of them.
         for (int i = 0; ok && i < cuts; ++i) {
           unsigned c0, c1;
           l.ctas_of(cut_u[i], c0, c1);
