@@ -175,7 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     reinterpret_cast<unsigned*>(g.err)[threadIdx.x] = 0u;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       Place<S> at;
       bool ok = true;
       const uint32_t fb0 = leader_addr(smem_u32(full)), base = smem_u32(smem);
@@ -209,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader && elect_one()) {
       const uint32_t idesc = idesc_bf16_f32_major(2 * kHalf, BN, AMN, BMN);
       Place<S> at;
       Place<2> acc;

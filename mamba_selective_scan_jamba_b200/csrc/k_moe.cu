@@ -175,6 +175,11 @@ struct Walk {
 // A place in a ring of n and the parity of its round.
 struct Place {
   unsigned s = 0, parity = 0;
+  __device__ __forceinline__ void skip(unsigned steps, unsigned n) {
+    const unsigned to = s + steps, rounds = to / n;
+    s = to - rounds * n;
+    parity ^= rounds & 1u;
+  }
   __device__ __forceinline__ void next(unsigned n) {
     if (++s == n) {
       s = 0;
@@ -543,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int epi_flag;
+  __shared__ int4 gather_rows[32];   // token rows of the block, 4 a gather
   Lists& L = *reinterpret_cast<Lists*>(smem + S * stage_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t tmem_cols = 64;   // two accumulators of two row groups
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         make_line(L.n_entries, a.D, a.F, 256, 1.0f)};
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t pol = l2_evict_first_policy();   // weights pass through once
       const uint32_t base = smem_u32(smem);
       Place at;
@@ -614,7 +620,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int ph = 0; ok && ph < 2; ++ph) {
       unsigned have = ~0u;   // the block whose h is known to be there, or whose rows are held
-      int t[4] = {};         // rows 4 lane .. 4 lane + 3 of the block
       for (Walk w(line[ph]); ok && w.more(); w.next()) {
         const Entry en = L.entry[w.ent];
         const int n16 = (en.n + 15) / 16;
@@ -622,8 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           have = w.ent;
           if (ph == 0) {
             // rows behind the last repeat it (their columns of the accumulator are not read)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) t[j] = L.token[en.r0 + min(lane * 4 + j, en.n - 1)];
+            __syncwarp();
+            const uint16_t* tok = L.token + en.r0;
+            const int r = lane * 4, last = en.n - 1;
+            gather_rows[lane] = make_int4(tok[min(r, last)], tok[min(r + 1, last)],
+                                          tok[min(r + 2, last)], tok[min(r + 3, last)]);
+            __syncwarp();
           } else {
             int there = 1;
             if (lane == 0)
@@ -632,31 +641,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
+            __syncwarp();
             fence_proxy_async_global();
           }
         }
-        int k = (int)w.k * kK;
-        for (unsigned n = w.steps(); n > 0; --n, k += kK, at.next(S)) {
-          // (every lane waits: each of them may issue a load into the stage)
-          ok = mbar_wait(smem_u32(&empty[at.s]), at.parity ^ 1u, a.err, 94);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = smem_u32(&full[at.s]), dst = base + at.s * stage_bytes;
-          if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(n16 * 16 * 128));
-          __syncwarp();
-          if (ph == 0) {
-            // 4 rows by index at a time: 16 rows of a block by 4 lanes
-            if (lane < n16 * 4) tma_gather4(dst + lane * 512, &tm_x, fb, k, t[0], t[1], t[2], t[3]);
-          } else if (lane < n16) {
-            tma_load_2d(dst + lane * 2048, &tm_h, fb, k, en.r0 + lane * 16);
+        int fail = 0;
+        if (elect_one()) {
+          int k = (int)w.k * kK;
+          Place p = at;
+          for (unsigned n = w.steps(); n > 0; --n, k += kK, p.next(S)) {
+            if (!mbar_wait(smem_u32(&empty[p.s]), p.parity ^ 1u, a.err, 94)) {
+              fail = 1;
+              break;
+            }
+            const uint32_t fb = smem_u32(&full[p.s]), dst = base + p.s * stage_bytes;
+            mbar_arrive_expect_tx(fb, (uint32_t)(n16 * 16 * 128));
+            if (ph == 0) {
+              for (int q = 0; q < n16 * 4; ++q) {   // 4 rows by index at a time
+                const int4 t = gather_rows[q];
+                tma_gather4(dst + q * 512, &tm_x, fb, k, t.x, t.y, t.z, t.w);
+              }
+            } else {
+              for (int q = 0; q < n16; ++q) tma_load_2d(dst + q * 2048, &tm_h, fb, k, en.r0 + q * 16);
+            }
           }
         }
+        at.skip(w.steps(), S);   // every lane keeps the place
+        ok = !__any_sync(0xffffffffu, fail);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t base = smem_u32(smem);
       Place at, acc;
       bool ok = true;
@@ -843,7 +858,7 @@ int moe_block(int64_t T, int64_t E, int64_t k) {
 }
 
 constexpr size_t kSmemMost = 227 * 1024;
-constexpr size_t kStaticMost = 512;   // barriers and flags
+constexpr size_t kStaticMost = 1024;  // barriers, flags and gather rows
 constexpr size_t kListBytes = (sizeof(Lists) + 255) / 256 * 256;
 
 int ring_stages(int nb) {
