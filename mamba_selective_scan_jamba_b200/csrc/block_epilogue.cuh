@@ -19,6 +19,12 @@ struct Epilogue {
   int act;
 };
 
+// The few-row products of k_linear_few.cu: C[T, N] = x [T, K] . w^T with the epilogue, w
+// stored [N, K], or [K, N] with w_mn.
+bool linear_few(int64_t M);
+cudaError_t run_linear_few(int64_t T, int64_t N, int64_t K, const void* x, const void* w, bool w_mn,
+                           const Epilogue& ep, ErrFlags* err, bool clear_err, Problem& p);
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);

@@ -627,7 +627,7 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int act, char* base) {
   w.gp = reinterpret_cast<__nv_bfloat16*>(take(act == JM_ACT_NONE ? 0 : (size_t)M * N * 2));
   const int64_t rows = M ? (M + gpre_rows(M, N) - 1) / gpre_rows(M, N) : 0;
   w.bias_part = reinterpret_cast<float*>(take((size_t)rows * N * 4));
-  const size_t px = M ? part_bytes(M, K, N) : 0, pw = M ? part_bytes(N, K, M) : 0;
+  const size_t px = M && !linear_few(M) ? part_bytes(M, K, N) : 0, pw = M ? part_bytes(N, K, M) : 0;
   w.part = reinterpret_cast<float*>(take(px > pw ? px : pw));
   w.bytes = off;
   return w;
@@ -636,7 +636,7 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int act, char* base) {
 }  // namespace
 
 size_t linear_fwd_ws_bytes(int64_t M, int64_t K, int64_t N) {
-  return sizeof(ErrFlags) + (M ? part_bytes(M, N, K) : 0);
+  return sizeof(ErrFlags) + (M && !linear_few(M) ? part_bytes(M, N, K) : 0);
 }
 
 size_t linear_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
@@ -653,6 +653,8 @@ cudaError_t run_linear_fwd(const LinearArgs& a, Problem& p) {
   ep.pre = static_cast<__nv_bfloat16*>(a.pre);
   ep.act = a.act;
   launches_begin(p);
+  if (linear_few(a.M))
+    return run_linear_few(a.M, a.N, a.K, a.x, a.w, false, ep, err, true, p);
   return product<false, false>(a.M, a.N, a.K, a.x, a.w, ep,
                                reinterpret_cast<float*>(a.ws + sizeof(ErrFlags)), err, true, p);
 }
@@ -695,7 +697,8 @@ cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
   ep.act = JM_ACT_NONE;
   if (a.g_x) {  // [M, K] = g_p [M, N] . w [N, K]
     ep.out = static_cast<__nv_bfloat16*>(a.g_x);
-    e = product<false, true>(a.M, a.K, a.N, gp, a.w, ep, w.part, err, clear, p);
+    e = linear_few(a.M) ? run_linear_few(a.M, a.K, a.N, gp, a.w, true, ep, err, clear, p)
+                        : product<false, true>(a.M, a.K, a.N, gp, a.w, ep, w.part, err, clear, p);
     if (e != cudaSuccess) return e;
   }
   if (a.g_w) {  // [N, K] = g_p [M, N]^T . x [M, K]

@@ -1,0 +1,325 @@
+// Linear layers of few rows on tcgen05 tensor cores, forward and the input's gradient:
+//   out[t, n] = act(sum_k x[t, k] w[n, k] + bias[n]) + residual[t, n]
+//   g_x[t, k] = sum_n g_p[t, n] w[n, k]
+//
+// With up to 256 rows the weights' bytes bound the product (one row of 4096 -> 16384:
+// 134 MB, 20 us of HBM time), so the weights are the MMA's A operand - 128 features are
+// the TMEM lanes - and the rows its N: no lane is wasted on rows that are not there, and
+// one row costs the tensor cores as little as 16.  In the gradient the contracted index
+// is the slow one of w, which tcgen05 takes as an MN-major A tile.
+//
+// A cluster of C CTAs shares a tile of 128 features, each a range of the contracted
+// index, so that few tiles still fill the GPU; their float32 tiles meet in shared memory
+// (no round trip through global memory, no second kernel): each CTA reads its share of
+// the columns from the others in rank order, so two runs give the same bits.
+#include <cuda.h>
+
+#include "block_epilogue.cuh"
+#include "jmix_internal.cuh"
+#include "sm100.cuh"
+
+namespace jmix {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 192;          // weights' and rows' producer, MMA, 4 drain warps
+constexpr int kK = 64;                 // K chunk: one 128-byte swizzle span
+constexpr int kTile = 128;             // features of a tile
+constexpr int kWBytes = kTile * kK * 2;
+constexpr int kMaxStages = 12;
+constexpr int kMaxCluster = 8;
+constexpr size_t kSmemSm = 227 * 1024;
+constexpr int64_t kFewRows = 128;      // above, k_linear_pair's 256-row tiles are not idle
+
+struct FewArgs {
+  int T, nb;             // rows; rounded up to the MMA's N
+  int chunks, stages;
+  unsigned tmem_cols;
+  int64_t N;             // features of the output
+  Epilogue ep;
+  ErrFlags* err;
+  bool clear_err;
+};
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t rank_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+
+// AMN: w is stored [contracted][features], else [features][contracted].
+template <bool AMN>
+__global__ void __launch_bounds__(kThreads)
+    k_linear_few(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                 const FewArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+  __shared__ uint32_t tmem_slot;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = g.stages, stage_bytes = kWBytes + g.nb * 128;
+  const uint32_t rank = cluster_rank(), C = cluster_size();
+  const int64_t n0 = (int64_t)(blockIdx.x / C) * kTile;
+  const int k0 = (int)((unsigned)g.chunks * rank / C), k1 = (int)((unsigned)g.chunks * (rank + 1) / C);
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(&done), 1);
+    fence_mbar_init();
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), g.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot, base = smem_u32(smem);
+  grid_dep_wait();
+  grid_dep_launch();
+  // (a wait gives up after 2 s: no CTA can have recorded one yet)
+  if (g.clear_err && blockIdx.x == 0 && tid < (int)(sizeof(ErrFlags) / 4))
+    reinterpret_cast<unsigned*>(g.err)[tid] = 0u;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      const uint64_t pol = l2_evict_first_policy();   // weights pass through once
+      int s = 0;
+      uint32_t parity = 1;   // the first round's wait for "empty" returns at once
+      for (int kc = k0; kc < k1; ++kc) {
+        if (!mbar_wait(smem_u32(&empty[s]), parity, g.err, 101)) break;
+        const uint32_t fb = smem_u32(&full[s]), dst = base + (uint32_t)(s * stage_bytes);
+        mbar_arrive_expect_tx(fb, (uint32_t)stage_bytes);
+        if constexpr (AMN) {   // boxes of 64 features x 64 contracted rows
+          tma_load_3d(dst, &tm_w, fb, (int32_t)n0, kc * kK, 0, pol);
+          tma_load_3d(dst + kWBytes / 2, &tm_w, fb, (int32_t)n0 + 64, kc * kK, 0, pol);
+        } else {
+          tma_load_3d(dst, &tm_w, fb, kc * kK, (int32_t)n0, 0, pol);
+        }
+        tma_load_2d(dst + kWBytes, &tm_x, fb, kc * kK, 0);
+        if (++s == S) {
+          s = 0;
+          parity ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      const uint32_t idesc = idesc_bf16_f32_major(kTile, g.nb, AMN, false);
+      int s = 0;
+      uint32_t parity = 0;
+      bool ok = true;
+      for (int kc = k0; kc < k1; ++kc) {
+        if (!mbar_wait(smem_u32(&full[s]), parity, g.err, 102)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t wa = base + (uint32_t)(s * stage_bytes), xb = wa + kWBytes;
+#pragma unroll
+        for (int kk = 0; kk < kK / 16; ++kk)
+          umma_f16(tmem,
+                   AMN ? sw128_mnmajor_desc(wa + kk * 2048, kWBytes / 2)
+                       : sw128_kmajor_desc(wa + kk * 32),
+                   sw128_kmajor_desc(xb + kk * 32), idesc, (kc > k0 || kk > 0) ? 1u : 0u);
+        umma_commit(smem_u32(&empty[s]));
+        if (++s == S) {
+          s = 0;
+          parity ^= 1u;
+        }
+      }
+      if (ok) umma_commit(smem_u32(&done));
+    }
+  }
+  // The tile [T][128] into the ring's place: all its loads were consumed by the MMAs.
+  float* tile = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+    const int lg = warp & 3, et = lg * 32 + lane;   // TMEM lane = feature of the tile
+    if (mbar_wait(smem_u32(&done), 0, g.err, 103)) {
+      tc_fence_after();
+      const uint32_t tb = tmem + ((uint32_t)(lg * 32) << 16);
+      for (int c = 0; c < g.T; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(tb + (uint32_t)c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c + i < g.T) tile[(c + i) * kTile + et] = __uint_as_float(r[i]);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();
+  // this CTA's share of the (row, 8 features) items
+  const unsigned items = (unsigned)g.T * (kTile / 8), i1 = items * (rank + 1) / C;
+  for (unsigned i = items * rank / C + tid; i < i1; i += kThreads) {
+    const unsigned t = i / (kTile / 8), f = i % (kTile / 8) * 8;
+    const int64_t col = n0 + f;
+    if (col >= g.N) continue;
+    const uint32_t at = base + (t * kTile + f) * 4;
+    const float4 l0 = *reinterpret_cast<const float4*>(tile + t * kTile + f);
+    const float4 l1 = *reinterpret_cast<const float4*>(tile + t * kTile + f + 4);
+    float v[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+    if (C > 1) {   // in rank order
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+#pragma unroll 4
+    for (uint32_t q = 0; C > 1 && q < C; ++q) {
+      const uint32_t p = rank_addr(at, q);
+      const float4 a = ld_cluster4(p), b = ld_cluster4(p + 16);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    finish8(g.ep, v, (int64_t)t * g.N + col, col);
+  }
+  cluster_sync();   // no CTA leaves while another may read its tile
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, g.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool map(CUtensorMap* m, const void* base, int64_t rows, int64_t inner, int box, int rank) {
+  const EncodeTiledFn fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)(inner * rows) * 2};
+  cuuint32_t bx[3] = {kK, (cuuint32_t)box, 1}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims,
+            strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How the product is cut: CTAs of a cluster, ring stages and shared memory of one.
+struct FewShape {
+  int nb, cluster, stages;
+  size_t smem;
+};
+
+// The least estimated time over cluster sizes and one or two CTAs an SM (two hide each
+// other's start and end and let up to 296 CTAs stream at once, with rings of half the
+// size).  An SM's rate for weights is what its rings hold over 1.2 us, a load's latency
+// from HBM under load; what passes through the SM, rows included, goes at 0.11 MB/us at
+// most; a wave of CTAs starts and ends in about 3 us, a cluster's two meetings in 1 to 2.
+FewShape few_shape(int64_t T, int64_t N, int64_t K) {
+  FewShape f{};
+  f.nb = (int)(ceil_div(T, 16) * 16);
+  const int64_t tiles = ceil_div(N, kTile), chunks = ceil_div(K, kK);
+  const size_t stage = kWBytes + (size_t)f.nb * 128, tile = (size_t)T * kTile * 4;
+  const double hbm = (double)N * (double)K * 2.0 / 6.5e6;
+  double best = 1e30;
+  for (int c = 1; c <= kMaxCluster; c *= 2) {
+    if (c > 1 && chunks / c < 2) break;
+    const int64_t ctas = tiles * c, steps = ceil_div(chunks, c);
+    for (int per = 1; per <= 2; ++per) {
+      const size_t most = kSmemSm / per - 3072;
+      int64_t stages = (int64_t)(most / stage);
+      if (stages < 3 || tile > most) break;
+      if (stages > kMaxStages) stages = kMaxStages;
+      if (stages > steps) stages = steps;
+      const int64_t waves = ceil_div(ctas, 148 * per);
+      const int64_t on_sm = ctas < 148 * per ? ceil_div(ctas, 148) : per;
+      const double latency = (double)steps / (double)stages * 1.2;
+      const double through = (double)(on_sm * steps) * (double)stage / 0.11e6;
+      double us = (double)waves * (latency > through ? latency : through);
+      if (us < hbm) us = hbm;
+      us += 3.0 * (double)waves + (c > 1 ? 1.0 + 0.1 * c : 0.0);
+      if (us < best * 0.98) {
+        best = us;
+        f.cluster = c;
+        f.stages = (int)stages;
+        const size_t ring = f.stages * stage;
+        f.smem = 1024 + (ring > tile ? ring : tile);
+      }
+    }
+  }
+  return f;
+}
+
+template <bool AMN>
+cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& x, const FewArgs& g,
+                       const FewShape& f, int64_t tiles, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(k_linear_few<AMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kSmemSm - 2048));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * f.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = f.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)f.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_linear_few<AMN>, w, x, g);
+}
+
+}  // namespace
+
+bool linear_few(int64_t M) { return M <= kFewRows; }
+
+cudaError_t run_linear_few(int64_t T, int64_t N, int64_t K, const void* x, const void* w, bool w_mn,
+                           const Epilogue& ep, ErrFlags* err, bool clear_err, Problem& p) {
+  const FewShape f = few_shape(T, N, K);
+  FewArgs g{};
+  g.T = (int)T;
+  g.nb = f.nb;
+  g.chunks = (int)ceil_div(K, kK);
+  g.stages = f.stages;
+  g.tmem_cols = 32;
+  while (g.tmem_cols < (unsigned)f.nb) g.tmem_cols *= 2;
+  g.N = N;
+  g.ep = ep;
+  g.err = err;
+  g.clear_err = clear_err;
+  CUtensorMap tw, tx;
+  if (!(w_mn ? map(&tw, w, K, N, 64, 3) : map(&tw, w, N, K, kTile, 3)) ||
+      !map(&tx, x, T, K, f.nb, 2))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = ceil_div(N, kTile);
+  const cudaError_t e = w_mn ? launch_few<true>(tw, tx, g, f, tiles, p.stream)
+                             : launch_few<false>(tw, tx, g, f, tiles, p.stream);
+  if (e == cudaSuccess) launched(p, "k_linear_few");
+  return e;
+}
+
+}  // namespace jmix
