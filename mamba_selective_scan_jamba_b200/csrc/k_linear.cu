@@ -11,16 +11,20 @@
 // tcgen05 takes either major order from a 128-byte-swizzled tile, so nothing is
 // transposed in memory.
 //
-// k_linear_pair: persistent CTA pairs (cluster of 2, cta_group::2), a 256 x BN tile
-// per pair, 64-wide K chunks in a TMA ring, the leader issues the MMAs, each CTA
-// drains its 128 rows from one of two accumulators while the next tile fills the
-// other.  Eight warps drain: a tile of 256 x 256 takes the tensor cores 17 us at K 4096
-// but 7 us at K 1744, and one warp for each quarter of the TMEM lanes needed 20 us with
-// an activation (6063 x 1744 x 8952 with SiLU: 322 us).  They stage 64 columns at a time
-// in swizzled shared memory; the residual comes into the same place by TMA before the
-// accumulator is complete, and TMA stores write whole lines.  Problems with few tiles are cut along K (`splits`): the work items write
-// float32 partial tiles and k_linear_reduce adds them in a fixed order and applies
-// the epilogue.
+// k_linear_pair: persistent CTA pairs (cta_group::2), a 256 x BN tile per pair, 64-wide K
+// chunks in a TMA ring, the leader issues the MMAs, each CTA drains its 128 rows from one
+// of two accumulators while the next tile fills the other.  Eight warps drain: a tile of
+// 256 x 256 takes the tensor cores 17 us at K 4096 but 7 us at K 1744, and one warp for
+// each quarter of the TMEM lanes needed 20 us with an activation (6063 x 1744 x 8952 with
+// SiLU: 322 us, with eight and staged stores 145 us).  They stage 64 columns at a time in
+// swizzled shared memory, two buffers a group; the residual comes into the same place by
+// TMA before the accumulator is complete, and TMA stores write whole lines.
+//
+// Problems with few tiles are cut along K.  Up to 4 pairs of a cluster share a tile
+// (`cpairs`): their float32 tiles meet in shared memory, each pair reads its share of the
+// columns from the others in rank order and finishes it.  Where more cuts pay
+// (`splits`), partial tiles go through global memory and k_linear_reduce adds them.
+// Products of up to 128 rows are k_linear_few's.
 #include <cuda.h>
 
 #include <atomic>
@@ -38,23 +42,39 @@ using namespace sm100;
 constexpr int kK = 64;              // K chunk: one 128-byte swizzle atom of bf16
 constexpr int kHalf = 128;          // tile rows per CTA
 constexpr int kThreads = 320;      // producer, MMA and 8 epilogue warps
-constexpr int kOutBytes = kHalf * 128;  // an epilogue group's staging: 128 rows x 128 bytes
+constexpr int kOutBytes = kHalf * 128;  // a staging buffer: 128 rows x 128 bytes
 constexpr int kGroupM = 16;         // row tiles per raster group
 constexpr uint32_t kTmemCols = 512;
 constexpr int kABytes = kHalf * kK * 2;                      // 16 KB
 constexpr int b_bytes(int BN) { return BN / 2 * kK * 2; }    // 16 or 8 KB
 constexpr int stage_bytes(int BN) { return kABytes + b_bytes(BN); }
-constexpr int stages(int BN) { return BN == 256 ? 6 : 7; }
-constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 2 * kOutBytes + 256; }
+constexpr int stages(int BN) { return BN == 256 ? 5 : 6; }
+constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 4 * kOutBytes + 256; }
 
 struct PairArgs {
   int64_t M, N, K;
   unsigned m_tiles, n_tiles;
-  int splits;    // above 1: float32 partial tiles [splits][M][N] through tm_out
+  int cpairs;    // pairs of a cluster, each a range of the tile's K
+  int splits;    // above 1 (cpairs 1): float32 partial tiles [splits][M][N] through tm_out
   Epilogue ep;   // (its out and residual are reached through the maps)
   ErrFlags* err;
   bool clear_err;  // the first kernel of a call clears the error header
 };
+
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 __device__ __forceinline__ void group_sync(int grp) {
   asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
@@ -97,9 +117,11 @@ __device__ __forceinline__ Item item_of(const PairArgs& g, unsigned w, int kchun
   it.mt = grp * kGroupM + idx - it.nt * rows;
   it.k0 = 0;
   it.k1 = kchunks;
-  if (g.splits > 1) {
-    it.k0 = (int)((int64_t)kchunks * it.split / g.splits);
-    it.k1 = (int)((int64_t)kchunks * (it.split + 1) / g.splits);
+  const int cuts = g.splits > 1 ? g.splits : g.cpairs;
+  if (cuts > 1) {
+    const int cut = g.splits > 1 ? (int)it.split : (int)(cluster_rank() >> 1);
+    it.k0 = (int)((int64_t)kchunks * cut / cuts);
+    it.k1 = (int)((int64_t)kchunks * (cut + 1) / cuts);
   }
   return it;
 }
@@ -118,8 +140,117 @@ struct Place {
   }
 };
 
+// What an epilogue group does with 64 columns (32 of a partial tile) of its rows.
+struct Drain {
+  const PairArgs& g;
+  uint8_t* stage;      // two buffers, used in turn
+  const int sw, grp;   // the swizzle of this thread's row
+  const uint32_t res_bar;
+  const int row_at;
+  const bool first;    // the thread that issues the group's copies
+  uint32_t res_parity = 0;
+  int buf = 0;
+  bool ok = true;
+
+  __device__ __forceinline__ Drain(const PairArgs& g, uint8_t* stage, uint32_t res_bar, int grp,
+                                   int r)
+      : g(g), stage(stage), sw(r & 7), grp(grp), res_bar(res_bar), row_at(r * 128),
+        first(r == 0) {}
+  __device__ __forceinline__ uint4* mine(int b) const {
+    return reinterpret_cast<uint4*>(stage + b * kOutBytes + row_at);
+  }
+  __device__ __forceinline__ uint32_t addr(int b) const {
+    return smem_u32(stage + b * kOutBytes);
+  }
+
+  // A buffer for the next chunk (with pre, which goes out first, both), and its residual.
+  __device__ __forceinline__ void open(const CUtensorMap& tm_res, int64_t col, int64_t row0) {
+    if (first) {
+      if (g.ep.pre)
+        bulk_wait_read<0>();
+      else
+        bulk_wait_read<1>();
+      if (ok && g.ep.residual && g.splits == 1) {
+        mbar_arrive_expect_tx(res_bar, kOutBytes);
+        tma_load_2d(addr(buf), &tm_res, res_bar, (int32_t)col, (int32_t)row0);
+      }
+    }
+    group_sync(grp);
+  }
+
+  __device__ __forceinline__ void partial(const CUtensorMap& tm_out, const uint32_t (&v)[64],
+                                          int64_t col, int64_t row0, unsigned split) {
+    uint4* m = mine(buf);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      m[i ^ sw] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    fence_proxy_async_smem();
+    group_sync(grp);
+    if (first) {
+      tma_store_3d(&tm_out, addr(buf), (int32_t)col, (int32_t)row0, (int32_t)split);
+      bulk_commit();
+    }
+    buf ^= 1;
+  }
+
+  __device__ __forceinline__ void finish(const CUtensorMap& tm_out, const CUtensorMap& tm_pre,
+                                         uint32_t (&v)[64], int64_t col, int64_t row0) {
+    if (g.ep.bias) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (col + 8 * i < g.N) {
+          float bv[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(g.ep.bias + col) + i), bv);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            v[8 * i + k] = __float_as_uint(__uint_as_float(v[8 * i + k]) + bv[k]);
+        }
+      }
+    }
+    if (g.ep.pre) {
+      uint4* m = mine(buf ^ 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i ^ sw] = pack8_bits(v + 8 * i);
+      fence_proxy_async_smem();
+      group_sync(grp);
+      if (first) {
+        tma_store_2d(&tm_pre, addr(buf ^ 1), (int32_t)col, (int32_t)row0);
+        bulk_commit();
+      }
+    }
+    if (g.ep.act != JM_ACT_NONE) apply_act(v, g.ep.act);
+    if (g.ep.residual) {
+      ok = ok && mbar_wait(res_bar, res_parity, g.err, 85);
+      res_parity ^= 1u;
+    }
+    uint4* m = mine(buf);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (g.ep.residual) {
+        float rv[8];
+        unpack8(m[i ^ sw], rv);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[8 * i + k] = __float_as_uint(__uint_as_float(v[8 * i + k]) + rv[k]);
+      }
+      m[i ^ sw] = pack8_bits(v + 8 * i);
+    }
+    fence_proxy_async_smem();
+    group_sync(grp);
+    if (first) {
+      tma_store_2d(&tm_out, addr(buf), (int32_t)col, (int32_t)row0);
+      bulk_commit();
+    }
+    buf ^= 1;
+  }
+
+  __device__ __forceinline__ void close() const {
+    if (first) bulk_wait_all();
+  }
+};
+
 template <bool AMN, bool BMN, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                   const __grid_constant__ CUtensorMap tm_out,
                   const __grid_constant__ CUtensorMap tm_res,
@@ -128,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* staging = smem + S * kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 2 * kOutBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 4 * kOutBytes);
   uint64_t* full = bars;              // [S] (leader) both CTAs' halves landed
   uint64_t* empty = bars + S;         // [S] the pair's MMAs have read the stage
   uint64_t* acc_full = bars + 2 * S;  // [2] accumulator complete
@@ -137,9 +268,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t crank = cluster_rank(), rank = crank & 1;   // rank in the pair
   const bool leader = rank == 0;
-  const unsigned pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  // (pairs of one cluster share a tile, and then a cluster has one)
+  const unsigned pair = blockIdx.x / (2 * g.cpairs), npairs = gridDim.x / (2 * g.cpairs);
   const unsigned items = g.m_tiles * g.n_tiles * g.splits;
   const int kchunks = (int)((g.K + kK - 1) / kK);
 
@@ -178,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       Place<S> at;
       bool ok = true;
-      const uint32_t fb0 = leader_addr(smem_u32(full)), base = smem_u32(smem);
+      const uint32_t fb0 = cluster_addr(smem_u32(full), crank & ~1u), base = smem_u32(smem);
       for (unsigned w = pair; ok && w < items; w += npairs) {
         const Item q = item_of(g, w, kchunks);
         const int32_t m0 = (int32_t)(q.mt * (2 * kHalf) + rank * kHalf);
@@ -211,6 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (leader && elect_one()) {
       const uint32_t idesc = idesc_bf16_f32_major(2 * kHalf, BN, AMN, BMN);
+      const uint16_t both = (uint16_t)(0x3u << crank);   // the pair's CTAs (crank is even here)
       Place<S> at;
       Place<2> acc;
       bool ok = true;
@@ -237,28 +370,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                     : sw128_kmajor_desc(bb + kk * 32);
             umma_f16_pair(d_tmem, ad, bd, idesc, (kc > q.k0 || kk > 0) ? 1u : 0u);
           }
-          umma_commit_pair(smem_u32(&empty[s]), 0x3);
+          umma_commit_pair(smem_u32(&empty[s]), both);
         }
-        if (ok) umma_commit_pair(smem_u32(&acc_full[b]), 0x3);
+        if (ok) umma_commit_pair(smem_u32(&acc_full[b]), both);
       }
     }
   } else {
     // epilogue: this CTA's 128 rows of the pair's 256-row tile, a row per thread; two
     // groups of 4 warps take the 128-byte column chunks in turn
     const int lg = warp & 3, grp = (warp - 2) >> 2, r = lg * 32 + lane;
-    const bool first = r == 0;
-    const bool split = g.splits > 1, act = g.ep.act != JM_ACT_NONE;
+    const bool split = g.splits > 1;
     const int cw = split ? 32 : 64;                   // columns in 128 bytes
-    const uint32_t acc_empty_leader = leader_addr(smem_u32(&acc_empty[0]));
-    uint8_t* stage = staging + grp * kOutBytes;
-    uint4* mine = reinterpret_cast<uint4*>(stage + r * 128);
-    const int sw = r & 7;                             // the swizzle of this row
-    const uint32_t res_bar = smem_u32(&res_full[grp]);
-    uint32_t res_phase = 0;
+    const uint32_t acc_empty_leader = cluster_addr(smem_u32(&acc_empty[0]), crank & ~1u);
+    Drain d(g, staging + grp * 2 * kOutBytes, smem_u32(&res_full[grp]), grp, r);
     Place<2> acc;
     // (a thread whose wait ran out goes on without waiting, so that its group's barriers
     // stay matched; the error header says that the values are not to be used)
-    bool ok = true;
     for (unsigned w = pair; w < items; w += npairs, acc.next()) {
       const Item q = item_of(g, w, kchunks);
       const int b = acc.s;
@@ -266,99 +393,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool rows = row0 < g.M;
       const uint32_t tbase = tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(b * 256);
       bool waited = false;
-      for (int c = grp * cw; rows && c < BN && n0 + c < g.N; c += 2 * cw) {
-        const int64_t col = n0 + c;
-        if (first) {
-          bulk_wait_read<0>();   // the staging is free
-          if (ok && !split && g.ep.residual) {
-            mbar_arrive_expect_tx(res_bar, kOutBytes);
-            tma_load_2d(smem_u32(stage), &tm_res, res_bar, (int32_t)col, (int32_t)row0);
-          }
-        }
-        group_sync(grp);
-        if (!waited) ok = ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
+      if (g.cpairs > 1) {
+        // the whole float32 tile into the ring's place (its MMAs are complete): 4 columns
+        // of all rows after one another, so that rows are 16 bytes apart
+        d.ok = d.ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
         waited = true;
         tc_fence_after();
-        uint32_t v[64];
-        if (split) {
+        float4* tile = reinterpret_cast<float4*>(smem) + r;
+        for (int c = grp * (BN / 2); c < (grp + 1) * (BN / 2); c += 32) {
+          uint32_t v[32];
           tmem_ld16(tbase + c, *reinterpret_cast<uint32_t(*)[16]>(v));
           tmem_ld16(tbase + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            mine[i ^ sw] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tmem_ld16(tbase + c + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(v + 16 * i));
-          tmem_ld_wait();
-          uint4 res[8];
-          if (g.ep.residual) {
-            ok = ok && mbar_wait(res_bar, res_phase, g.err, 85);
-            res_phase ^= 1u;
-            if (g.ep.pre)   // the staging holds pre first
-#pragma unroll
-              for (int i = 0; i < 8; ++i) res[i] = mine[i ^ sw];
-          }
-          if (g.ep.bias) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (col + 8 * i < g.N) {
-                float bv[8];
-                unpack8(__ldg(reinterpret_cast<const uint4*>(g.ep.bias + col) + i), bv);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  v[8 * i + k] = __float_as_uint(__uint_as_float(v[8 * i + k]) + bv[k]);
-              }
-            }
-          }
-          if (g.ep.pre) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mine[i ^ sw] = pack8_bits(v + 8 * i);
-            fence_proxy_async_smem();
-            group_sync(grp);
-            if (first) {
-              tma_store_2d(&tm_pre, smem_u32(stage), (int32_t)col, (int32_t)row0);
-              bulk_commit();
-              bulk_wait_read<0>();
-            }
-            group_sync(grp);
-          }
-          if (act) {
-            apply_act(v, g.ep.act);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (g.ep.residual) {
-              float rv[8];
-              unpack8(g.ep.pre ? res[i] : mine[i ^ sw], rv);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                v[8 * i + k] = __float_as_uint(__uint_as_float(v[8 * i + k]) + rv[k]);
-            }
-            mine[i ^ sw] = pack8_bits(v + 8 * i);
-          }
+            tile[(c / 4 + i) * kHalf] =
+                make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                            __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
         }
-        fence_proxy_async_smem();
-        group_sync(grp);
-        if (first) {
-          if (split)
-            tma_store_3d(&tm_out, smem_u32(stage), (int32_t)col, (int32_t)row0, (int32_t)q.split);
-          else
-            tma_store_2d(&tm_out, smem_u32(stage), (int32_t)col, (int32_t)row0);
-          bulk_commit();
+        break;   // one tile per cluster; it is finished below
+      }
+      for (int c = grp * cw; rows && c < BN && n0 + c < g.N; c += 2 * cw) {
+        const int64_t col = n0 + c;
+        d.open(tm_res, col, row0);
+        if (!waited) d.ok = d.ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
+        waited = true;
+        tc_fence_after();
+        uint32_t v[64];
+        tmem_ld16(tbase + c, *reinterpret_cast<uint32_t(*)[16]>(v));
+        tmem_ld16(tbase + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+        if (split) {
+          tmem_ld_wait();
+          d.partial(tm_out, v, col, row0, q.split);
+        } else {
+          tmem_ld16(tbase + c + 32, *reinterpret_cast<uint32_t(*)[16]>(v + 32));
+          tmem_ld16(tbase + c + 48, *reinterpret_cast<uint32_t(*)[16]>(v + 48));
+          tmem_ld_wait();
+          d.finish(tm_out, tm_pre, v, col, row0);
         }
       }
       // the accumulator is free once it is complete and this warp has read its part
-      if (!waited) ok = ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
+      if (!waited) d.ok = d.ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty_leader + (uint32_t)(b * 8));
     }
-    if (first) bulk_wait_all();
+    if (g.cpairs == 1) d.close();
+  }
+  if (g.cpairs > 1) {
+    tc_fence_before();
+    cluster_sync();   // the cluster's tiles are all there
+    if (warp >= 2) {
+      const int grp = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;
+      Drain d(g, staging + grp * 2 * kOutBytes, smem_u32(&res_full[grp]), grp, r);
+      const Item q = item_of(g, pair, kchunks);
+      const int64_t row0 = (int64_t)q.mt * (2 * kHalf) + rank * kHalf;
+      // this pair's columns: BN / cpairs of them, 64 at a time
+      const int cols = BN / g.cpairs, c0 = (int)(crank >> 1) * cols;
+      for (int c = c0 + grp * 64; c < c0 + cols; c += 128) {
+        const int64_t col = (int64_t)q.nt * BN + c;
+        if (row0 >= g.M || col >= g.N) break;
+        d.open(tm_res, col, row0);
+        uint32_t v[64];
+        const uint32_t at = smem_u32(smem) + (uint32_t)((c / 4) * kHalf + r) * 16;
+        for (int p = 0; p < g.cpairs; ++p) {
+          const uint32_t from = cluster_addr(at, 2 * p + rank);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float4 f = ld_cluster4(from + i * kHalf * 16);
+            const float o[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[4 * i + k] = __float_as_uint(p ? __uint_as_float(v[4 * i + k]) + o[k] : o[k]);
+          }
+        }
+        d.finish(tm_out, tm_pre, v, col, row0);
+      }
+      d.close();
+    }
   }
   tc_fence_before();
-  cluster_sync();   // no CTA leaves while its pair may still signal it
+  cluster_sync();   // no CTA leaves while another may still signal it or read its tile
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
@@ -474,29 +589,41 @@ bool part_map(CUtensorMap* m, const void* base, int64_t splits, int64_t M, int64
 
 constexpr int kPairs = 74;   // CTA pairs of a B200 (148 SMs)
 
-// How a product is cut: tile width and K splits.
+// How a product is cut: tile width, pairs of a cluster on a tile, K splits through memory.
 struct Cut {
-  int bn, splits;
+  int bn, cpairs, splits;
 };
 
 // Estimated microseconds: waves of work items on 74 pairs (a 64-wide chunk of a 256 x
-// 256 tile takes a pair 0.4 us, of a 256 x 128 tile 0.23), ~2 us for the first fill and
-// last drain, and for splits the partial tiles' round trip through L2 and one launch.
+// 256 tile takes a pair 0.27 us, of a 256 x 128 tile 0.16), ~2 us for the first fill and
+// last drain; 2 us for a cluster's exchange; for splits the partial tiles' round trip
+// through L2 and one launch.
 Cut choose_cut(int64_t M, int64_t N, int64_t K) {
   const int64_t chunks = (K + kK - 1) / kK;
-  Cut best{256, 1};
+  Cut best{256, 1, 1};
   double best_us = 1e30;
   for (int bn = 256; bn >= 128; bn /= 2) {
     const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn);
-    const double chunk_us = bn == 256 ? 0.40 : 0.23;
+    const double chunk_us = bn == 256 ? 0.27 : 0.16;
     for (int s = 1; s <= 16; ++s) {
-      if (s > 1 && chunks / s < 4) break;
+      if (s > 1 && chunks / s < 2) break;
       const int64_t waves = (tiles * s + kPairs - 1) / kPairs;
-      double us = (double)waves * (double)((chunks + s - 1) / s) * chunk_us + 2.0;
-      if (s > 1) us += 3.0 + (double)M * (double)N * 4.0 * (2 * s + 1) / 6.0e6;
-      if (us < best_us * 0.999) {
-        best_us = us;
-        best = {bn, s};
+      const double us = (double)waves * (double)((chunks + s - 1) / s) * chunk_us + 2.0;
+      // (a cluster's pairs take equal shares of at least 64 columns; a B200 holds 33 clusters
+      // of 4 CTAs or 15 of 8 with one CTA an SM)
+      if (s == 1 || (s == 2 && tiles <= 33) || (s == 4 && bn == 256 && tiles <= 15)) {
+        const double c = us + (s > 1 ? 2.0 : 0.0);
+        if (c < best_us * 0.999) {
+          best_us = c;
+          best = {bn, s, 1};
+        }
+      }
+      if (s > 1) {
+        const double m = us + 5.0 + (double)M * (double)N * 4.0 * (2 * s + 1) / 6.0e6;
+        if (m < best_us * 0.999) {
+          best_us = m;
+          best = {bn, 1, s};
+        }
       }
     }
   }
@@ -525,24 +652,33 @@ int query_pairs() {
   cfg.gridDim = dim3(2 * kPairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes(BN);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
   return n;
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                   Args... args) {
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                   cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
@@ -555,9 +691,9 @@ cudaError_t launch_pair(const CUtensorMap (&tm)[5], const PairArgs& g, cudaStrea
   const int most = cached_attr(cache, dev, query_pairs<AMN, BMN, BN>);
   if (most <= 0) return cudaErrorInvalidConfiguration;
   const int64_t items = (int64_t)g.m_tiles * g.n_tiles * g.splits;
-  const int64_t pairs = items < most ? items : most;
-  return launch(k_linear_pair<AMN, BMN, BN>, dim3((unsigned)(2 * pairs)), dim3(kThreads),
-                (size_t)smem_bytes(BN), s, tm[0], tm[1], tm[2], tm[3], tm[4], g);
+  const int64_t clusters = items < most || g.cpairs > 1 ? items : most;
+  return launch(k_linear_pair<AMN, BMN, BN>, dim3((unsigned)(2 * g.cpairs * clusters)),
+                dim3(kThreads), (size_t)smem_bytes(BN), 2 * g.cpairs, s, tm[0], tm[1], tm[2], tm[3], tm[4], g);
 }
 
 // C[M, N] = A . B^T with the epilogue `ep`.  AMN / BMN: A is stored [K, M], B [K, N].
@@ -580,6 +716,7 @@ cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* 
   g.K = K;
   g.m_tiles = (unsigned)((M + 255) / 256);
   g.n_tiles = (unsigned)((N + c.bn - 1) / c.bn);
+  g.cpairs = c.cpairs;
   g.splits = c.splits;
   g.ep = ep;
   g.err = err;
@@ -591,7 +728,7 @@ cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* 
   if (c.splits > 1) {
     const int64_t n = M * N / 8;
     const int64_t ctas = (n + 255) / 256 < 148 * 8 ? (n + 255) / 256 : 148 * 8;
-    e = launch(k_linear_reduce, dim3((unsigned)ctas), dim3(256), 0, p.stream, (const float*)part,
+    e = launch(k_linear_reduce, dim3((unsigned)ctas), dim3(256), 0, 1, p.stream, (const float*)part,
                c.splits, M, N, ep);
     if (e == cudaSuccess) launched(p, "k_linear_reduce");
   }
@@ -675,7 +812,7 @@ cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
   if (grad || a.g_bias) {
     const int rows = gpre_rows(a.M, a.N);
     const dim3 grid((unsigned)((a.N + kGpCols - 1) / kGpCols), (unsigned)((a.M + rows - 1) / rows));
-    e = launch(k_linear_gpre, grid, dim3(256), 0, p.stream,
+    e = launch(k_linear_gpre, grid, dim3(256), 0, 1, p.stream,
                static_cast<const __nv_bfloat16*>(a.g_out),
                grad ? static_cast<const __nv_bfloat16*>(a.pre) : nullptr, a.act, a.M, a.N, rows,
                w.gp, a.g_bias ? w.bias_part : nullptr, err);
@@ -683,7 +820,7 @@ cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
     launched(p, "k_linear_gpre");
     if (grad) gp = w.gp;
     if (a.g_bias) {
-      e = launch(k_linear_bias_reduce, dim3((unsigned)((a.N + 31) / 32)), dim3(32, 16), 0, p.stream,
+      e = launch(k_linear_bias_reduce, dim3((unsigned)((a.N + 31) / 32)), dim3(32, 16), 0, 1, p.stream,
                  (const float*)w.bias_part, (int64_t)grid.y, a.N,
                  static_cast<__nv_bfloat16*>(a.g_bias));
       if (e != cudaSuccess) return e;

@@ -230,6 +230,9 @@ struct FewShape {
 // from HBM under load; what passes through the SM, rows included, goes at 0.11 MB/us at
 // most; a wave of CTAs starts and ends in about 3 us, a cluster's two meetings in 1 to 2.
 FewShape few_shape(int64_t T, int64_t N, int64_t K) {
+  // clusters of 1, 2, 4 and 8 CTAs that a B200 holds, with one or two CTAs an SM
+  static const int kClusters[2][9] = {{0, 148, 74, 0, 33, 0, 0, 0, 15},
+                                      {0, 296, 148, 0, 71, 0, 0, 0, 33}};
   FewShape f{};
   f.nb = (int)(ceil_div(T, 16) * 16);
   const int64_t tiles = ceil_div(N, kTile), chunks = ceil_div(K, kK);
@@ -245,7 +248,7 @@ FewShape few_shape(int64_t T, int64_t N, int64_t K) {
       if (stages < 3 || tile > most) break;
       if (stages > kMaxStages) stages = kMaxStages;
       if (stages > steps) stages = steps;
-      const int64_t waves = ceil_div(ctas, 148 * per);
+      const int64_t waves = ceil_div(tiles, kClusters[per - 1][c]);
       const int64_t on_sm = ctas < 148 * per ? ceil_div(ctas, 148) : per;
       const double latency = (double)steps / (double)stages * 1.2;
       const double through = (double)(on_sm * steps) * (double)stage / 0.11e6;
