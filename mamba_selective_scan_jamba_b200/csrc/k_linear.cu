@@ -48,8 +48,16 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kABytes = kHalf * kK * 2;                      // 16 KB
 constexpr int b_bytes(int BN) { return BN / 2 * kK * 2; }    // 16 or 8 KB
 constexpr int stage_bytes(int BN) { return kABytes + b_bytes(BN); }
-constexpr int stages(int BN) { return BN == 256 ? 5 : 6; }
-constexpr int smem_bytes(int BN) { return 1024 + stages(BN) * stage_bytes(BN) + 4 * kOutBytes + 256; }
+// Ring stages and staging share 224 KB.  A CTA with one tile has nothing to drain while its
+// ring is in use: its ring takes all of it and the staging the ring's place afterwards
+// (loads from HBM take 1.4 us under load, five stages of a 0.27 us step).
+constexpr int kRegion = 224 * 1024;
+constexpr int kMaxStages = kRegion / stage_bytes(128);
+constexpr int kStaging = 4 * kOutBytes;
+constexpr int stages(int BN, bool single) {
+  return (single ? kRegion : kRegion - kStaging) / stage_bytes(BN);
+}
+constexpr int kSmemBytes = 1024 + kRegion + 8 * (2 * kMaxStages + 6) + 16;
 
 struct PairArgs {
   int64_t M, N, K;
@@ -58,6 +66,7 @@ struct PairArgs {
   int splits;    // above 1 (cpairs 1): float32 partial tiles [splits][M][N] through tm_out
   Epilogue ep;   // (its out and residual are reached through the maps)
   ErrFlags* err;
+  bool single;     // no CTA has two tiles
   bool clear_err;  // the first kernel of a call clears the error header
 };
 
@@ -128,12 +137,12 @@ __device__ __forceinline__ Item item_of(const PairArgs& g, unsigned w, int kchun
 
 // A place in the ring and the parity of its round: counted on, since a division by the
 // number of stages in each step of one thread's loop is time that the loads do not have.
-template <int S>
 struct Place {
-  int s = 0;
+  int n, s = 0;
   uint32_t parity = 0;
+  __device__ __forceinline__ explicit Place(int n) : n(n) {}
   __device__ __forceinline__ void next() {
-    if (++s == S) {
+    if (++s == n) {
       s = 0;
       parity ^= 1u;
     }
@@ -255,14 +264,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tm_out,
                   const __grid_constant__ CUtensorMap tm_res,
                   const __grid_constant__ CUtensorMap tm_pre, const PairArgs g) {
-  constexpr int S = stages(BN), kStage = stage_bytes(BN), kBHalf = BN / 2;
+  constexpr int kStage = stage_bytes(BN), kBHalf = BN / 2;
+  const int S = stages(BN, g.single);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* staging = smem + S * kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 4 * kOutBytes);
+  // (behind the float32 tile that a cluster's pairs exchange)
+  uint8_t* staging = g.single ? smem + (g.cpairs > 1 ? BN * kHalf * 4 : 0) : smem + S * kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRegion);
   uint64_t* full = bars;              // [S] (leader) both CTAs' halves landed
-  uint64_t* empty = bars + S;         // [S] the pair's MMAs have read the stage
-  uint64_t* acc_full = bars + 2 * S;  // [2] accumulator complete
+  uint64_t* empty = full + kMaxStages;  // [S] the pair's MMAs have read the stage
+  uint64_t* acc_full = empty + kMaxStages;  // [2] accumulator complete
   uint64_t* acc_empty = acc_full + 2; // [2] (leader) both epilogues are done (16 warps)
   uint64_t* res_full = acc_empty + 2; // [2] a group's residual box landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 2);
@@ -308,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (elect_one()) {
-      Place<S> at;
+      Place at(S);
       bool ok = true;
       const uint32_t fb0 = cluster_addr(smem_u32(full), crank & ~1u), base = smem_u32(smem);
       for (unsigned w = pair; ok && w < items; w += npairs) {
@@ -344,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader && elect_one()) {
       const uint32_t idesc = idesc_bf16_f32_major(2 * kHalf, BN, AMN, BMN);
       const uint16_t both = (uint16_t)(0x3u << crank);   // the pair's CTAs (crank is even here)
-      Place<S> at;
-      Place<2> acc;
+      Place at(S);
+      Place acc(2);
       bool ok = true;
       const uint32_t base = smem_u32(smem);
       for (unsigned w = pair; ok && w < items; w += npairs, acc.next()) {
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = split ? 32 : 64;                   // columns in 128 bytes
     const uint32_t acc_empty_leader = cluster_addr(smem_u32(&acc_empty[0]), crank & ~1u);
     Drain d(g, staging + grp * 2 * kOutBytes, smem_u32(&res_full[grp]), grp, r);
-    Place<2> acc;
+    Place acc(2);
     // (a thread whose wait ran out goes on without waiting, so that its group's barriers
     // stay matched; the error header says that the values are not to be used)
     for (unsigned w = pair; w < items; w += npairs, acc.next()) {
@@ -415,9 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int c = grp * cw; rows && c < BN && n0 + c < g.N; c += 2 * cw) {
         const int64_t col = n0 + c;
-        d.open(tm_res, col, row0);
+        if (!g.single) d.open(tm_res, col, row0);
         if (!waited) d.ok = d.ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
         waited = true;
+        if (g.single) d.open(tm_res, col, row0);   // the staging was the ring's until now
         tc_fence_after();
         uint32_t v[64];
         tmem_ld16(tbase + c, *reinterpret_cast<uint32_t(*)[16]>(v));
@@ -645,13 +657,13 @@ int cached_attr(std::atomic<int>* cache, int dev, int (*query)()) {
 template <bool AMN, bool BMN, int BN>
 int query_pairs() {
   auto kern = k_linear_pair<AMN, BMN, BN>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN)) !=
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
       cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * kPairs);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(BN);
+  cfg.dynamicSmemBytes = kSmemBytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -691,9 +703,9 @@ cudaError_t launch_pair(const CUtensorMap (&tm)[5], const PairArgs& g, cudaStrea
   const int most = cached_attr(cache, dev, query_pairs<AMN, BMN, BN>);
   if (most <= 0) return cudaErrorInvalidConfiguration;
   const int64_t items = (int64_t)g.m_tiles * g.n_tiles * g.splits;
-  const int64_t clusters = items < most || g.cpairs > 1 ? items : most;
+  const int64_t clusters = g.single || items < most ? items : most;
   return launch(k_linear_pair<AMN, BMN, BN>, dim3((unsigned)(2 * g.cpairs * clusters)),
-                dim3(kThreads), (size_t)smem_bytes(BN), 2 * g.cpairs, s, tm[0], tm[1], tm[2], tm[3], tm[4], g);
+                dim3(kThreads), (size_t)kSmemBytes, 2 * g.cpairs, s, tm[0], tm[1], tm[2], tm[3], tm[4], g);
 }
 
 // C[M, N] = A . B^T with the epilogue `ep`.  AMN / BMN: A is stored [K, M], B [K, N].
@@ -720,6 +732,7 @@ cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* 
   g.splits = c.splits;
   g.ep = ep;
   g.err = err;
+  g.single = (int64_t)g.m_tiles * g.n_tiles * g.splits <= kPairs || c.cpairs > 1;
   g.clear_err = clear_err;
   cudaError_t e = c.bn == 256 ? launch_pair<AMN, BMN, 256>(tm, g, p.stream)
                               : launch_pair<AMN, BMN, 128>(tm, g, p.stream);
