@@ -122,7 +122,7 @@ struct NormBwdArgs {
   void* g_x;
   float* part;           // partial rows of g_w and g_b, or null
   ErrFlags* err;
-  int wpr, rpc;
+  int wpr, rpc, stages;
 };
 size_t norm_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t x_stride, jm_dtype io);
 cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p);

@@ -20,7 +20,10 @@
 // 16 bytes).  In the backward a group walks over rows with a stride, so that each
 // thread owns its columns of g_w and g_b and sums them in registers; the groups'
 // partial rows go to the workspace and k_norm_bwd_reduce adds them in a fixed
-// order (the same bits on every run).
+// order (the same bits on every run).  k_norm_bwd_ring has the rows of g_y, x and g_sum
+// copied into a ring in shared memory some rows ahead (with loads of the next row only,
+// 8192 x 4096 bf16 with g_sum took 109 us); k_norm_bwd loads them itself, for rows that
+// bulk copies cannot take (not multiples of 16 bytes) or that no ring has room for.
 #include "jmix_internal.cuh"
 #include "sm100.cuh"
 
@@ -31,6 +34,7 @@ using sm100::grid_dep_launch;
 using sm100::grid_dep_wait;
 
 constexpr int kNormSMs = 148;
+constexpr int kNormMaxStages = 6;
 
 template <typename T, int VEC>
 struct RawT {
@@ -316,9 +320,162 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) k_norm_bwd(const No
   }
 }
 
+// The backward with its rows copied ahead.  A round takes the CTA's next rpc rows; the
+// stage they came from is refilled for the round `stages` later at the round's barrier,
+// when every thread holds its values in registers.
+template <typename T, int VEC, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(const NormBwdArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][2][32];
+  __shared__ uint64_t full[kNormMaxStages];
+  using R = Raw<T, VEC>;
+  const int gthreads = 32 * a.wpr;
+  const int group = threadIdx.x / gthreads, t = threadIdx.x - group * gthreads;
+  const int nvec = (int)(a.cols / VEC), S = a.stages;
+  const uint32_t row_bytes = (uint32_t)(a.cols * sizeof(T)), part_bytes = row_bytes * a.rpc;
+  const uint32_t stage_bytes = part_bytes * (a.g_sum ? 3 : 2);
+  const int64_t step = (int64_t)gridDim.x * a.rpc, first = (int64_t)blockIdx.x * a.rpc;
+  const int64_t rounds = (a.rows - first + step - 1) / step;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) sm100::mbar_init(sm100::smem_u32(&full[i]), 1);
+    sm100::fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x == 0 && threadIdx.x < sizeof(ErrFlags) / 4)
+    reinterpret_cast<unsigned*>(a.err)[threadIdx.x] = 0u;
+  auto fill = [&](int64_t it, int s) {   // one thread
+    const int64_t row = first + it * step, left = a.rows - row;
+    const uint32_t n = left < a.rpc ? (uint32_t)left : (uint32_t)a.rpc;
+    const uint32_t bar = sm100::smem_u32(&full[s]);
+    uint32_t dst = sm100::smem_u32(ring) + s * stage_bytes;
+    sm100::mbar_arrive_expect_tx(bar, n * row_bytes * (a.g_sum ? 3 : 2));
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    if (a.x_stride == a.cols)
+      sm100::bulk_load(dst, x, n * row_bytes, bar);
+    else
+      for (uint32_t i = 0; i < n; ++i)
+        sm100::bulk_load(dst + i * row_bytes, x + i * a.x_stride, row_bytes, bar);
+    sm100::bulk_load(dst + part_bytes, static_cast<const T*>(a.gy) + row * a.cols, n * row_bytes,
+                     bar);
+    if (a.g_sum)
+      sm100::bulk_load(dst + 2 * part_bytes, static_cast<const T*>(a.g_sum) + row * a.cols,
+                       n * row_bytes, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < S && i < rounds; ++i) fill(i, i);
+  const R* wp = static_cast<const R*>(a.weight);
+  R rw[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = v * gthreads + t;
+    rw[v] = i < nvec ? wp[i] : zero_raw<R>();
+  }
+  float gw[NV][VEC], gb[NV][VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) gw[v][j] = gb[v][j] = 0.0f;
+  const float inv_n = 1.0f / (float)a.cols;
+  const float2* stats = reinterpret_cast<const float2*>(a.stats);
+  float2 st = first + group < a.rows ? stats[first + group] : make_float2(0.0f, 0.0f);
+  int s = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  for (int64_t it = 0; it < rounds; ++it) {
+    const int64_t row = first + it * step + group;
+    const bool live = row < a.rows;
+    const float mean = st.x, rs = st.y;
+    if (row + step < a.rows) st = stats[row + step];
+    ok = ok && sm100::mbar_wait(sm100::smem_u32(&full[s]), parity, a.err, 111);
+    const R* src = reinterpret_cast<const R*>(ring + s * stage_bytes) + group * nvec;
+    float xh[NV][VEC], g[NV][VEC];
+    R rs_sum[NV];
+    float sg = 0.0f, sgx = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = v * gthreads + t;
+      const bool in = live && i < nvec;
+      const R rx = in ? src[i] : zero_raw<R>();
+      const R rg = in ? src[i + nvec * a.rpc] : zero_raw<R>();
+      rs_sum[v] = in && a.g_sum ? src[i + 2 * nvec * a.rpc] : zero_raw<R>();
+      float w[VEC];
+      unpack<T, VEC>(rx, xh[v]);
+      unpack<T, VEC>(rg, g[v]);
+      unpack<T, VEC>(rw[v], w);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        xh[v][j] = in ? (xh[v][j] - mean) * rs : 0.0f;
+        gw[v][j] = fmaf(g[v][j], xh[v][j], gw[v][j]);
+        gb[v][j] += g[v][j];
+        g[v][j] *= w[j];
+        sg += g[v][j];
+        sgx = fmaf(g[v][j], xh[v][j], sgx);
+      }
+    }
+    sg = warp_sum(sg);
+    sgx = warp_sum(sgx);
+    float(*rd)[32] = red[it & 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (a.wpr > 1 && lane == 0) {
+      rd[0][warp] = sg;
+      rd[1][warp] = sgx;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && ok && it + S < rounds) fill(it + S, s);
+    if (++s == S) {
+      s = 0;
+      parity ^= 1u;
+    }
+    if (a.wpr > 1) {
+      const int w0 = warp / a.wpr * a.wpr;
+      sg = warp_sum(lane < a.wpr ? rd[0][w0 + lane] : 0.0f);
+      sgx = warp_sum(lane < a.wpr ? rd[1][w0 + lane] : 0.0f);
+    }
+    const float c0 = a.layer ? sg * inv_n : 0.0f, c1 = sgx * inv_n;
+    if (live) {
+      R* gx = static_cast<R*>(a.g_x) + row * nvec;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int i = v * gthreads + t;
+        if (i >= nvec) break;
+        float o[VEC], q[VEC];
+        unpack<T, VEC>(rs_sum[v], q);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o[j] = fmaf(g[v][j] - c0 - xh[v][j] * c1, rs, q[j]);
+        gx[i] = pack<T, VEC>(o);
+      }
+    }
+  }
+  if (a.part) {
+    // the groups' sums, added in their order: one partial row a CTA
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ring);   // [rpc][2][cols]
+    float* mine = sums + (int64_t)group * 2 * a.cols;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = v * gthreads + t;
+      if (i >= nvec) break;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        mine[i * VEC + j] = gw[v][j];
+        mine[a.cols + i * VEC + j] = gb[v][j];
+      }
+    }
+    __syncthreads();
+    float* pw = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+    for (int c = threadIdx.x; c < 2 * (int)a.cols; c += blockDim.x) {
+      float acc = sums[c];
+      for (int q = 1; q < a.rpc; ++q) acc += sums[(int64_t)q * 2 * a.cols + c];
+      pw[c] = acc;
+    }
+  }
+}
+
 // g_w (blockIdx.y = 0) and g_b (1): the partial rows of 32 columns, added in a
 // fixed order.
-constexpr int kRedRows = 16;
+constexpr int kRedRows = 32;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kRedRows)
@@ -333,6 +490,7 @@ __global__ void __launch_bounds__(32 * kRedRows)
   float acc = 0.0f;
   if (c < cols) {
     const float* p = part + blockIdx.y * cols + c;
+#pragma unroll 4
     for (int64_t r = threadIdx.y; r < n_part; r += kRedRows) acc += p[r * 2 * cols];
   }
   sh[threadIdx.y][threadIdx.x] = acc;
@@ -367,11 +525,12 @@ NormShape norm_shape(int64_t cols, int64_t x_stride, jm_dtype io) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t s,
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, size_t smem,
                        Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -408,10 +567,37 @@ NormKern<NormBwdArgs> bwd_kernel(const NormShape& s, jm_dtype io) {
 }
 #undef JMIX_NORM_PICK
 
+NormKern<NormBwdArgs> ring_kernel(const NormShape& s, jm_dtype io) {
+  if (io == JM_BF16)
+    return s.threads() <= 256   ? k_norm_bwd_ring<__nv_bfloat16, 8, 2, 256>
+           : s.threads() <= 512 ? k_norm_bwd_ring<__nv_bfloat16, 8, 2, 512>
+                                : k_norm_bwd_ring<__nv_bfloat16, 8, 2, 1024>;
+  return s.threads() <= 256   ? k_norm_bwd_ring<float, 4, 2, 256>
+         : s.threads() <= 512 ? k_norm_bwd_ring<float, 4, 2, 512>
+                              : k_norm_bwd_ring<float, 4, 2, 1024>;
+}
+
+// Stages of the backward's ring (at least 2), or 0 where the loading kernel runs: rows that
+// are no multiple of 16 bytes, or too long for two stages.  CTAs of 256 threads share an SM
+// in pairs.
+int ring_stages(int64_t cols, bool g_sum, const NormShape& s, jm_dtype io) {
+  if (s.vec == 1 || s.nv != 2) return 0;
+  const size_t stage = (size_t)(s.rpc * cols) * (io == JM_BF16 ? 2 : 4) * (g_sum ? 3 : 2);
+  const size_t most = s.threads() <= 256 ? 110 * 1024 : 220 * 1024;
+  const int n = (int)(most / stage);
+  return n < 2 ? 0 : n < kNormMaxStages ? n : kNormMaxStages;
+}
+
+size_t ring_bytes(int64_t cols, bool g_sum, int stages, const NormShape& s, jm_dtype io) {
+  const size_t ring = (size_t)stages * (s.rpc * cols) * (io == JM_BF16 ? 2 : 4) * (g_sum ? 3 : 2);
+  const size_t sums = (size_t)s.rpc * 2 * cols * 4;
+  return ring > sums ? ring : sums;
+}
+
 // CTAs of the backward: as many as are resident at once, so that there are few
 // partial rows to add.
-int64_t bwd_ctas(int64_t rows, const NormShape& s) {
-  const int64_t most = (int64_t)kNormSMs * (s.threads() <= 256 ? 3 : 1);
+int64_t bwd_ctas(int64_t rows, const NormShape& s, bool ring) {
+  const int64_t most = (int64_t)kNormSMs * (s.threads() > 256 ? 1 : ring ? 2 : 3);
   const int64_t need = (rows + s.rpc - 1) / s.rpc;
   return need < most ? need : most;
 }
@@ -420,7 +606,7 @@ int64_t bwd_ctas(int64_t rows, const NormShape& s) {
 
 size_t norm_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t x_stride, jm_dtype io) {
   const NormShape s = norm_shape(cols, x_stride, io);
-  return sizeof(ErrFlags) + align256((size_t)(bwd_ctas(rows, s) * s.rpc * 2 * cols) * 4);
+  return sizeof(ErrFlags) + align256((size_t)(bwd_ctas(rows, s, false) * s.rpc * 2 * cols) * 4);
 }
 
 cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p) {
@@ -430,7 +616,7 @@ cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p) {
   const int64_t ctas = (a.rows + s.rpc - 1) / s.rpc;
   launches_begin(p);
   const cudaError_t e = launch_pdl(fwd_kernel(s, io), dim3((unsigned)ctas), dim3(s.threads()),
-                                   p.stream, a);
+                                   p.stream, 0, a);
   if (e == cudaSuccess) launched(p, "k_norm_fwd");
   return e;
 }
@@ -443,24 +629,35 @@ cudaError_t run_norm_bwd(NormBwdArgs a, void* g_w, void* g_b, char* ws, jm_dtype
   const bool sums = g_w || g_b;
   float* part = reinterpret_cast<float*>(ws + sizeof(ErrFlags));
   a.part = sums ? part : nullptr;
-  const int64_t ctas = bwd_ctas(a.rows, s);
+  a.stages = ring_stages(a.cols, a.g_sum != nullptr, s, io);
+  const int64_t ctas = bwd_ctas(a.rows, s, a.stages > 0);
+  const int64_t part_rows = a.stages > 0 ? ctas : ctas * s.rpc;
   cudaError_t e = cudaSuccess;
   launches_begin(p);
-  if (ctas > 0) {
-    e = launch_pdl(bwd_kernel(s, io), dim3((unsigned)ctas), dim3(s.threads()), p.stream, a);
+  if (ctas == 0) {
+    e = cudaMemsetAsync(ws, 0, sizeof(ErrFlags), p.stream);
+  } else if (a.stages > 0) {
+    const NormKern<NormBwdArgs> kern = ring_kernel(s, io);
+    // (a flag of the function on the current device; setting it again costs a few tenths
+    // of a microsecond)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    if (e == cudaSuccess)
+      e = launch_pdl(kern, dim3((unsigned)ctas), dim3(s.threads()), p.stream,
+                     ring_bytes(a.cols, a.g_sum != nullptr, a.stages, s, io), a);
     if (e == cudaSuccess) launched(p, "k_norm_bwd");
   } else {
-    e = cudaMemsetAsync(ws, 0, sizeof(ErrFlags), p.stream);
+    e = launch_pdl(bwd_kernel(s, io), dim3((unsigned)ctas), dim3(s.threads()), p.stream, 0, a);
+    if (e == cudaSuccess) launched(p, "k_norm_bwd");
   }
   if (e == cudaSuccess && sums) {
     const dim3 grid((unsigned)((a.cols + 31) / 32), 2);
     if (io == JM_BF16)
-      e = launch_pdl(k_norm_bwd_reduce<__nv_bfloat16>, grid, dim3(32, kRedRows), p.stream,
-                     (const float*)part, ctas * s.rpc, a.cols, static_cast<__nv_bfloat16*>(g_w),
+      e = launch_pdl(k_norm_bwd_reduce<__nv_bfloat16>, grid, dim3(32, kRedRows), p.stream, 0,
+                     (const float*)part, part_rows, a.cols, static_cast<__nv_bfloat16*>(g_w),
                      static_cast<__nv_bfloat16*>(g_b));
     else
-      e = launch_pdl(k_norm_bwd_reduce<float>, grid, dim3(32, kRedRows), p.stream,
-                     (const float*)part, ctas * s.rpc, a.cols, static_cast<float*>(g_w),
+      e = launch_pdl(k_norm_bwd_reduce<float>, grid, dim3(32, kRedRows), p.stream, 0,
+                     (const float*)part, part_rows, a.cols, static_cast<float*>(g_w),
                      static_cast<float*>(g_b));
     if (e == cudaSuccess) launched(p, "k_norm_bwd_reduce");
   }
