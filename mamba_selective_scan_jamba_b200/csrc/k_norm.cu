@@ -22,8 +22,9 @@
 // partial rows go to the workspace and k_norm_bwd_reduce adds them in a fixed
 // order (the same bits on every run).  k_norm_bwd_ring has the rows of g_y, x and g_sum
 // copied into a ring in shared memory some rows ahead (with loads of the next row only,
-// 8192 x 4096 bf16 with g_sum took 109 us); k_norm_bwd loads them itself, for rows that
-// bulk copies cannot take (not multiples of 16 bytes) or that no ring has room for.
+// 8192 x 4096 bf16 with g_sum took 109 us, with the ring 51 us); k_norm_bwd loads them
+// itself, for rows of x that lie apart by no multiple of 16 bytes and rows that no ring has
+// room for.
 #include "jmix_internal.cuh"
 #include "sm100.cuh"
 
@@ -320,6 +321,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) k_norm_bwd(const No
   }
 }
 
+// Shared memory of one array's rows in a stage of the backward's ring.
+__host__ __device__ inline uint32_t ring_part_bytes(size_t rows_bytes, bool ragged) {
+  return (uint32_t)(ragged ? (rows_bytes + 15) / 16 * 16 + 16 : rows_bytes);
+}
+
 // The backward with its rows copied ahead.  A round takes the CTA's next rpc rows; the
 // stage they came from is refilled for the round `stages` later at the round's barrier,
 // when every thread holds its values in registers.
@@ -332,8 +338,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
   const int gthreads = 32 * a.wpr;
   const int group = threadIdx.x / gthreads, t = threadIdx.x - group * gthreads;
   const int nvec = (int)(a.cols / VEC), S = a.stages;
-  const uint32_t row_bytes = (uint32_t)(a.cols * sizeof(T)), part_bytes = row_bytes * a.rpc;
+  const uint32_t row_bytes = (uint32_t)(a.cols * sizeof(T));
+  const uint32_t part_bytes = ring_part_bytes(a.rpc * (size_t)row_bytes, VEC == 1);
   const uint32_t stage_bytes = part_bytes * (a.g_sum ? 3 : 2);
+  // Rows that are no multiple of 16 bytes (VEC 1) come with what is around them up to the
+  // next 16-byte boundaries; behind `safe` they would end outside the tensor.
+  const int64_t safe = a.rows * row_bytes & ~int64_t(15);
   const int64_t step = (int64_t)gridDim.x * a.rpc, first = (int64_t)blockIdx.x * a.rpc;
   const int64_t rounds = (a.rows - first + step - 1) / step;
   if (threadIdx.x == 0) {
@@ -350,6 +360,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
     const uint32_t n = left < a.rpc ? (uint32_t)left : (uint32_t)a.rpc;
     const uint32_t bar = sm100::smem_u32(&full[s]);
     uint32_t dst = sm100::smem_u32(ring) + s * stage_bytes;
+    if constexpr (VEC == 1) {
+      const int64_t r0 = row * row_bytes & ~int64_t(15);
+      const int64_t r1 = min((row + n) * row_bytes + 15 & ~int64_t(15), safe);
+      const uint32_t bytes = r1 > r0 ? (uint32_t)(r1 - r0) : 0u;
+      sm100::mbar_arrive_expect_tx(bar, bytes * (a.g_sum ? 3 : 2));
+      if (bytes == 0) return;
+      sm100::bulk_load(dst, static_cast<const char*>(a.x) + r0, bytes, bar);
+      sm100::bulk_load(dst + part_bytes, static_cast<const char*>(a.gy) + r0, bytes, bar);
+      if (a.g_sum)
+        sm100::bulk_load(dst + 2 * part_bytes, static_cast<const char*>(a.g_sum) + r0, bytes, bar);
+      return;
+    }
     sm100::mbar_arrive_expect_tx(bar, n * row_bytes * (a.g_sum ? 3 : 2));
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     if (a.x_stride == a.cols)
@@ -389,7 +411,26 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
     const float mean = st.x, rs = st.y;
     if (row + step < a.rows) st = stats[row + step];
     ok = ok && sm100::mbar_wait(sm100::smem_u32(&full[s]), parity, a.err, 111);
-    const R* src = reinterpret_cast<const R*>(ring + s * stage_bytes) + group * nvec;
+    uint8_t* stage = ring + s * stage_bytes;
+    uint32_t at = (uint32_t)group * row_bytes;
+    if constexpr (VEC == 1) {
+      const int64_t r0 = first + it * step, from = r0 * row_bytes & ~int64_t(15);
+      at = (uint32_t)(row * row_bytes - from);
+      if (r0 + a.rpc >= a.rows && safe < a.rows * row_bytes) {   // (uniform in the CTA)
+        // the values behind `safe`, at most 7 of each array
+        const int n = (int)((a.rows * row_bytes - safe) / sizeof(T)), q = threadIdx.x;
+        if (q < n * (a.g_sum ? 3 : 2)) {
+          const int k = q / n;
+          const void* array = k == 0 ? a.x : k == 1 ? a.gy : a.g_sum;
+          reinterpret_cast<T*>(stage + k * part_bytes + (safe - from))[q - k * n] =
+              reinterpret_cast<const T*>(static_cast<const char*>(array) + safe)[q - k * n];
+        }
+        __syncthreads();
+      }
+    }
+    const R* sx = reinterpret_cast<const R*>(stage + at);
+    const R* sgy = reinterpret_cast<const R*>(stage + part_bytes + at);
+    const R* ssum = reinterpret_cast<const R*>(stage + 2 * part_bytes + at);
     float xh[NV][VEC], g[NV][VEC];
     R rs_sum[NV];
     float sg = 0.0f, sgx = 0.0f;
@@ -397,9 +438,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
     for (int v = 0; v < NV; ++v) {
       const int i = v * gthreads + t;
       const bool in = live && i < nvec;
-      const R rx = in ? src[i] : zero_raw<R>();
-      const R rg = in ? src[i + nvec * a.rpc] : zero_raw<R>();
-      rs_sum[v] = in && a.g_sum ? src[i + 2 * nvec * a.rpc] : zero_raw<R>();
+      const R rx = in ? sx[i] : zero_raw<R>();
+      const R rg = in ? sgy[i] : zero_raw<R>();
+      rs_sum[v] = in && a.g_sum ? ssum[i] : zero_raw<R>();
       float w[VEC];
       unpack<T, VEC>(rx, xh[v]);
       unpack<T, VEC>(rg, g[v]);
@@ -514,12 +555,13 @@ NormShape norm_shape(int64_t cols, int64_t x_stride, jm_dtype io) {
   const int full = io == JM_BF16 ? 8 : 4;
   s.vec = cols % full == 0 && x_stride % full == 0 ? full : 1;
   const int64_t nvec = cols / s.vec;
-  // the fewest warps that hold the row at 2 (scalar: 4) vectors a thread, and
-  // more vectors a thread only where 32 warps are not enough
-  s.nv = s.vec > 1 ? 2 : 4;
+  // the fewest warps that hold the row at 2 vectors a thread (more only where 32 warps
+  // are not enough), or single values at 4 or, above 512, 16 a thread (with 4, a row of
+  // 3141 took 1024 threads, two CTAs an SM: 554 rows 11.4 us)
+  s.nv = s.vec > 1 ? 2 : cols <= 512 ? 4 : 16;
   s.wpr = 1;
   while (s.wpr < 32 && (int64_t)32 * s.wpr * s.nv < nvec) s.wpr *= 2;
-  if ((int64_t)32 * s.wpr * s.nv < nvec) s.nv = s.vec > 1 ? 4 : 16;
+  if ((int64_t)32 * s.wpr * s.nv < nvec) s.nv = 4;
   s.rpc = s.wpr >= 8 ? 1 : 8 / s.wpr;  // CTAs of 256 threads, or one wider row
   return s;
 }
@@ -545,16 +587,16 @@ using NormKern = void (*)(const Args);
 
 // The kernel built for a shape's threads (rounded up to 256, 512 or 1024, which
 // sets the registers a thread may use).  16,384 columns need 4 vectors a thread
-// only in float32 and 16 values only in scalar form, both at 1024 threads.
+// only in float32, at 1024 threads; 4 single values a thread are for 512 columns at most.
 #define JMIX_NORM_PICK(KERN, T, FULL)                                                   \
   (s.vec > 1 ? (s.nv == 4             ? KERN<T, FULL, 16 / FULL, 1024>                  \
                 : s.threads() <= 256  ? KERN<T, FULL, 2, 256>                           \
                 : s.threads() <= 512  ? KERN<T, FULL, 2, 512>                           \
                                       : KERN<T, FULL, 2, 1024>)                         \
-             : (s.nv == 16            ? KERN<T, 1, 16, 1024>                            \
-                : s.threads() <= 256  ? KERN<T, 1, 4, 256>                              \
-                : s.threads() <= 512  ? KERN<T, 1, 4, 512>                              \
-                                      : KERN<T, 1, 4, 1024>))
+             : (s.nv == 4             ? KERN<T, 1, 4, 256>                              \
+                : s.threads() <= 256  ? KERN<T, 1, 16, 256>                             \
+                : s.threads() <= 512  ? KERN<T, 1, 16, 512>                             \
+                                      : KERN<T, 1, 16, 1024>))
 
 NormKern<NormFwdArgs> fwd_kernel(const NormShape& s, jm_dtype io) {
   if (io == JM_BF16) return JMIX_NORM_PICK(k_norm_fwd, __nv_bfloat16, 8);
@@ -567,29 +609,39 @@ NormKern<NormBwdArgs> bwd_kernel(const NormShape& s, jm_dtype io) {
 }
 #undef JMIX_NORM_PICK
 
-NormKern<NormBwdArgs> ring_kernel(const NormShape& s, jm_dtype io) {
-  if (io == JM_BF16)
-    return s.threads() <= 256   ? k_norm_bwd_ring<__nv_bfloat16, 8, 2, 256>
-           : s.threads() <= 512 ? k_norm_bwd_ring<__nv_bfloat16, 8, 2, 512>
-                                : k_norm_bwd_ring<__nv_bfloat16, 8, 2, 1024>;
-  return s.threads() <= 256   ? k_norm_bwd_ring<float, 4, 2, 256>
-         : s.threads() <= 512 ? k_norm_bwd_ring<float, 4, 2, 512>
-                              : k_norm_bwd_ring<float, 4, 2, 1024>;
+template <typename T, int FULL>
+NormKern<NormBwdArgs> ring_kernel_of(const NormShape& s) {
+  if (s.vec > 1)
+    return s.threads() <= 256   ? k_norm_bwd_ring<T, FULL, 2, 256>
+           : s.threads() <= 512 ? k_norm_bwd_ring<T, FULL, 2, 512>
+                                : k_norm_bwd_ring<T, FULL, 2, 1024>;
+  if (s.nv == 4) return k_norm_bwd_ring<T, 1, 4, 256>;
+  return s.threads() <= 256   ? k_norm_bwd_ring<T, 1, 16, 256>
+         : s.threads() <= 512 ? k_norm_bwd_ring<T, 1, 16, 512>
+                              : k_norm_bwd_ring<T, 1, 16, 1024>;
 }
 
-// Stages of the backward's ring (at least 2), or 0 where the loading kernel runs: rows that
-// are no multiple of 16 bytes, or too long for two stages.  CTAs of 256 threads share an SM
-// in pairs.
-int ring_stages(int64_t cols, bool g_sum, const NormShape& s, jm_dtype io) {
-  if (s.vec == 1 || s.nv != 2) return 0;
-  const size_t stage = (size_t)(s.rpc * cols) * (io == JM_BF16 ? 2 : 4) * (g_sum ? 3 : 2);
+NormKern<NormBwdArgs> ring_kernel(const NormShape& s, jm_dtype io) {
+  return io == JM_BF16 ? ring_kernel_of<__nv_bfloat16, 8>(s) : ring_kernel_of<float, 4>(s);
+}
+
+size_t ring_stage(int64_t cols, bool g_sum, const NormShape& s, jm_dtype io) {
+  return (size_t)ring_part_bytes((size_t)s.rpc * cols * (io == JM_BF16 ? 2 : 4), s.vec == 1) *
+         (g_sum ? 3 : 2);
+}
+
+// Stages of the backward's ring (at least 2), or 0 where the loading kernel runs: rows of
+// x apart by no multiple of 16 bytes, or too long for two stages.  CTAs of 256 threads share
+// an SM in pairs.
+int ring_stages(int64_t cols, int64_t x_stride, bool g_sum, const NormShape& s, jm_dtype io) {
+  if ((s.vec == 1 && x_stride != cols) || (s.vec > 1 && s.nv != 2)) return 0;
   const size_t most = s.threads() <= 256 ? 110 * 1024 : 220 * 1024;
-  const int n = (int)(most / stage);
+  const int n = (int)(most / ring_stage(cols, g_sum, s, io));
   return n < 2 ? 0 : n < kNormMaxStages ? n : kNormMaxStages;
 }
 
 size_t ring_bytes(int64_t cols, bool g_sum, int stages, const NormShape& s, jm_dtype io) {
-  const size_t ring = (size_t)stages * (s.rpc * cols) * (io == JM_BF16 ? 2 : 4) * (g_sum ? 3 : 2);
+  const size_t ring = stages * ring_stage(cols, g_sum, s, io);
   const size_t sums = (size_t)s.rpc * 2 * cols * 4;
   return ring > sums ? ring : sums;
 }
@@ -629,7 +681,7 @@ cudaError_t run_norm_bwd(NormBwdArgs a, void* g_w, void* g_b, char* ws, jm_dtype
   const bool sums = g_w || g_b;
   float* part = reinterpret_cast<float*>(ws + sizeof(ErrFlags));
   a.part = sums ? part : nullptr;
-  a.stages = ring_stages(a.cols, a.g_sum != nullptr, s, io);
+  a.stages = ring_stages(a.cols, a.x_stride, a.g_sum != nullptr, s, io);
   const int64_t ctas = bwd_ctas(a.rows, s, a.stages > 0);
   const int64_t part_rows = a.stages > 0 ? ctas : ctas * s.rpc;
   cudaError_t e = cudaSuccess;
