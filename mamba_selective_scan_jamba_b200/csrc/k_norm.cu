@@ -16,8 +16,7 @@
 // the gradients are rounded once to the io type.
 //
 // A group of `wpr` warps owns a row; a thread keeps NV vectors of VEC values
-// (16-byte accesses; VEC = 1 where the width or the stride is not a multiple of
-// 16 bytes).  In the backward a group walks over rows with a stride, so that each
+// (16-byte accesses, or 8, 4 or 2 where the width or the stride of x asks for them).  In the backward a group walks over rows with a stride, so that each
 // thread owns its columns of g_w and g_b and sums them in registers; the groups'
 // partial rows go to the workspace and k_norm_bwd_reduce adds them in a fixed
 // order (the same bits on every run).  k_norm_bwd_ring has the rows of g_y, x and g_sum
@@ -37,32 +36,51 @@ using sm100::grid_dep_wait;
 constexpr int kNormSMs = 148;
 constexpr int kNormMaxStages = 6;
 
-template <typename T, int VEC>
-struct RawT {
-  using type = uint4;
-};
-template <typename T>
-struct RawT<T, 1> {
+// VEC values as one access: 16, 8 or 4 bytes, or a single value.
+template <typename T, int VEC, int BYTES>
+struct RawOf {
   using type = T;
 };
 template <typename T, int VEC>
-using Raw = typename RawT<T, VEC>::type;
+struct RawOf<T, VEC, 16> {
+  using type = uint4;
+};
+template <typename T, int VEC>
+struct RawOf<T, VEC, 8> {
+  using type = uint2;
+};
+template <>
+struct RawOf<__nv_bfloat16, 2, 4> {
+  using type = uint32_t;
+};
+template <typename T, int VEC>
+using Raw = typename RawOf<T, VEC, VEC * sizeof(T)>::type;
 
 template <typename T, int VEC>
 __device__ __forceinline__ void unpack(const Raw<T, VEC>& r, float (&f)[VEC]) {
   if constexpr (VEC == 1) {
     f[0] = static_cast<float>(r);
-  } else if constexpr (sizeof(T) == 4) {
-    f[0] = __uint_as_float(r.x);
-    f[1] = __uint_as_float(r.y);
-    f[2] = __uint_as_float(r.z);
-    f[3] = __uint_as_float(r.w);
   } else {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+    constexpr int W = VEC * sizeof(T) / 4;
+    uint32_t u[W];
+    if constexpr (W == 1) {
+      u[0] = r;
+    } else {
+      u[0] = r.x;
+      u[1] = r.y;
+      if constexpr (W == 4) {
+        u[2] = r.z;
+        u[3] = r.w;
+      }
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < W; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f[i] = __uint_as_float(u[i]);
+      } else {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
     }
   }
 }
@@ -71,17 +89,24 @@ template <typename T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> pack(const float (&f)[VEC]) {
   if constexpr (VEC == 1) {
     return static_cast<T>(f[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
   } else {
-    uint32_t u[4];
+    constexpr int W = VEC * sizeof(T) / 4;
+    uint32_t u[W];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t*>(&v);
+    for (int i = 0; i < W; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        u[i] = __float_as_uint(f[i]);
+      } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
     }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    if constexpr (W == 1)
+      return u[0];
+    else if constexpr (W == 2)
+      return make_uint2(u[0], u[1]);
+    else
+      return make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
@@ -89,8 +114,10 @@ template <typename R>
 __device__ __forceinline__ R zero_raw() {
   if constexpr (sizeof(R) == 16)
     return make_uint4(0u, 0u, 0u, 0u);
+  else if constexpr (sizeof(R) == 8)
+    return make_uint2(0u, 0u);
   else
-    return static_cast<R>(0.0f);
+    return R{};
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -335,13 +362,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
   __shared__ float red[2][2][32];
   __shared__ uint64_t full[kNormMaxStages];
   using R = Raw<T, VEC>;
+  constexpr bool kRagged = VEC * sizeof(T) < 16;
   const int gthreads = 32 * a.wpr;
   const int group = threadIdx.x / gthreads, t = threadIdx.x - group * gthreads;
   const int nvec = (int)(a.cols / VEC), S = a.stages;
   const uint32_t row_bytes = (uint32_t)(a.cols * sizeof(T));
-  const uint32_t part_bytes = ring_part_bytes(a.rpc * (size_t)row_bytes, VEC == 1);
+  const uint32_t part_bytes = ring_part_bytes(a.rpc * (size_t)row_bytes, kRagged);
   const uint32_t stage_bytes = part_bytes * (a.g_sum ? 3 : 2);
-  // Rows that are no multiple of 16 bytes (VEC 1) come with what is around them up to the
+  // Rows that are no multiple of 16 bytes come with what is around them up to the
   // next 16-byte boundaries; behind `safe` they would end outside the tensor.
   const int64_t safe = a.rows * row_bytes & ~int64_t(15);
   const int64_t step = (int64_t)gridDim.x * a.rpc, first = (int64_t)blockIdx.x * a.rpc;
@@ -360,7 +388,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
     const uint32_t n = left < a.rpc ? (uint32_t)left : (uint32_t)a.rpc;
     const uint32_t bar = sm100::smem_u32(&full[s]);
     uint32_t dst = sm100::smem_u32(ring) + s * stage_bytes;
-    if constexpr (VEC == 1) {
+    if constexpr (kRagged) {
       const int64_t r0 = row * row_bytes & ~int64_t(15);
       const int64_t r1 = min((row + n) * row_bytes + 15 & ~int64_t(15), safe);
       const uint32_t bytes = r1 > r0 ? (uint32_t)(r1 - r0) : 0u;
@@ -413,7 +441,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
     ok = ok && sm100::mbar_wait(sm100::smem_u32(&full[s]), parity, a.err, 111);
     uint8_t* stage = ring + s * stage_bytes;
     uint32_t at = (uint32_t)group * row_bytes;
-    if constexpr (VEC == 1) {
+    if constexpr (kRagged) {
       const int64_t r0 = first + it * step, from = r0 * row_bytes & ~int64_t(15);
       at = (uint32_t)(row * row_bytes - from);
       if (r0 + a.rpc >= a.rows && safe < a.rows * row_bytes) {   // (uniform in the CTA)
@@ -547,21 +575,32 @@ __global__ void __launch_bounds__(32 * kRedRows)
 // per row and rows per CTA.
 struct NormShape {
   int vec, nv, wpr, rpc;
+  bool full;   // 16-byte vectors
   int threads() const { return 32 * wpr * rpc; }
+  int ring_ctas() const { return threads() > 256 ? 1 : threads() > 160 ? 2 : 3; }   // of an SM
 };
 
-NormShape norm_shape(int64_t cols, int64_t x_stride, jm_dtype io) {
+// `narrow`: 8- and 4-byte vectors too (else single values where 16 bytes do not fit).
+NormShape norm_shape(int64_t cols, int64_t x_stride, jm_dtype io, bool narrow) {
   NormShape s;
   const int full = io == JM_BF16 ? 8 : 4;
-  s.vec = cols % full == 0 && x_stride % full == 0 ? full : 1;
+  s.vec = full;
+  while (s.vec > 1 && (cols % s.vec || x_stride % s.vec)) s.vec = narrow ? s.vec / 2 : 1;
+  s.full = s.vec == full;
   const int64_t nvec = cols / s.vec;
-  // the fewest warps that hold the row at 2 vectors a thread (more only where 32 warps
-  // are not enough), or single values at 4 or, above 512, 16 a thread (with 4, a row of
-  // 3141 took 1024 threads, two CTAs an SM: 554 rows 11.4 us)
-  s.nv = s.vec > 1 ? 2 : cols <= 512 ? 4 : 16;
-  s.wpr = 1;
-  while (s.wpr < 32 && (int64_t)32 * s.wpr * s.nv < nvec) s.wpr *= 2;
-  if ((int64_t)32 * s.wpr * s.nv < nvec) s.nv = 4;
+  // The fewest warps that hold the row at 2 vectors of 16 bytes a thread (more only where
+  // 32 warps are not enough), or of narrower ones at 4, 8 or 16 values a thread: up to 512
+  // columns as many as let one warp hold the row (16000 x 332: 11.2 us, with 3 warps and
+  // their barriers 18.2 us), then 8 (816 x 943: 5.2 us, with 16 6.6 us), above 2048 16
+  // (554 x 3141: 7.3 us, with 4 and 1024 threads 11.4 us).
+  const int values = cols <= 128 ? 4 : cols <= 256 ? 8 : cols <= 512 ? 16 : cols <= 2048 ? 8 : 16;
+  s.nv = s.full ? 2 : values / s.vec;
+  int64_t wpr = (nvec + 32 * s.nv - 1) / (32 * s.nv);
+  if (wpr > 32) {
+    s.nv = 4;     // float32 above 8192 columns
+    wpr = (nvec + 127) / 128;
+  }
+  s.wpr = (int)wpr;
   s.rpc = s.wpr >= 8 ? 1 : 8 / s.wpr;  // CTAs of 256 threads, or one wider row
   return s;
 }
@@ -585,57 +624,64 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream
 template <typename Args>
 using NormKern = void (*)(const Args);
 
-// The kernel built for a shape's threads (rounded up to 256, 512 or 1024, which
-// sets the registers a thread may use).  16,384 columns need 4 vectors a thread
-// only in float32, at 1024 threads; 4 single values a thread are for 512 columns at most.
-#define JMIX_NORM_PICK(KERN, T, FULL)                                                   \
-  (s.vec > 1 ? (s.nv == 4             ? KERN<T, FULL, 16 / FULL, 1024>                  \
-                : s.threads() <= 256  ? KERN<T, FULL, 2, 256>                           \
-                : s.threads() <= 512  ? KERN<T, FULL, 2, 512>                           \
-                                      : KERN<T, FULL, 2, 1024>)                         \
-             : (s.nv == 4             ? KERN<T, 1, 4, 256>                              \
-                : s.threads() <= 256  ? KERN<T, 1, 16, 256>                             \
-                : s.threads() <= 512  ? KERN<T, 1, 16, 512>                             \
-                                      : KERN<T, 1, 16, 1024>))
+// The kernel built for a shape's threads (rounded up to 256, 512 or 1024, which sets the
+// registers a thread may use).  16,384 columns need 4 vectors of 16 bytes a thread only in
+// float32, at 1024 threads; 4 and 8 values in narrower ones are for 128 and 2048 columns.
+#define JMIX_NORM_FULL(KERN, T, FULL)                             \
+  (s.nv == 4             ? KERN<T, FULL, 16 / FULL, 1024>         \
+   : s.threads() <= 256  ? KERN<T, FULL, 2, 256>                  \
+   : s.threads() <= 512  ? KERN<T, FULL, 2, 512>                  \
+                         : KERN<T, FULL, 2, 1024>)
+#define JMIX_NORM_NARROW(KERN, T, VEC)                            \
+  (s.nv * VEC == 4       ? KERN<T, VEC, 4 / VEC, 256>             \
+   : s.nv * VEC == 8     ? KERN<T, VEC, 8 / VEC, 256>             \
+   : s.threads() <= 256  ? KERN<T, VEC, 16 / VEC, 256>            \
+   : s.threads() <= 512  ? KERN<T, VEC, 16 / VEC, 512>            \
+                         : KERN<T, VEC, 16 / VEC, 1024>)
 
 NormKern<NormFwdArgs> fwd_kernel(const NormShape& s, jm_dtype io) {
-  if (io == JM_BF16) return JMIX_NORM_PICK(k_norm_fwd, __nv_bfloat16, 8);
-  return JMIX_NORM_PICK(k_norm_fwd, float, 4);
-}
-
-NormKern<NormBwdArgs> bwd_kernel(const NormShape& s, jm_dtype io) {
-  if (io == JM_BF16) return JMIX_NORM_PICK(k_norm_bwd, __nv_bfloat16, 8);
-  return JMIX_NORM_PICK(k_norm_bwd, float, 4);
-}
-#undef JMIX_NORM_PICK
-
-template <typename T, int FULL>
-NormKern<NormBwdArgs> ring_kernel_of(const NormShape& s) {
-  if (s.vec > 1)
-    return s.threads() <= 256   ? k_norm_bwd_ring<T, FULL, 2, 256>
-           : s.threads() <= 512 ? k_norm_bwd_ring<T, FULL, 2, 512>
-                                : k_norm_bwd_ring<T, FULL, 2, 1024>;
-  if (s.nv == 4) return k_norm_bwd_ring<T, 1, 4, 256>;
-  return s.threads() <= 256   ? k_norm_bwd_ring<T, 1, 16, 256>
-         : s.threads() <= 512 ? k_norm_bwd_ring<T, 1, 16, 512>
-                              : k_norm_bwd_ring<T, 1, 16, 1024>;
+  if (io == JM_BF16) {
+    if (s.full) return JMIX_NORM_FULL(k_norm_fwd, __nv_bfloat16, 8);
+    return s.vec == 4   ? JMIX_NORM_NARROW(k_norm_fwd, __nv_bfloat16, 4)
+           : s.vec == 2 ? JMIX_NORM_NARROW(k_norm_fwd, __nv_bfloat16, 2)
+                        : JMIX_NORM_NARROW(k_norm_fwd, __nv_bfloat16, 1);
+  }
+  if (s.full) return JMIX_NORM_FULL(k_norm_fwd, float, 4);
+  return s.vec == 2 ? JMIX_NORM_NARROW(k_norm_fwd, float, 2)
+                    : JMIX_NORM_NARROW(k_norm_fwd, float, 1);
 }
 
 NormKern<NormBwdArgs> ring_kernel(const NormShape& s, jm_dtype io) {
-  return io == JM_BF16 ? ring_kernel_of<__nv_bfloat16, 8>(s) : ring_kernel_of<float, 4>(s);
+  if (io == JM_BF16) {
+    if (s.full) return JMIX_NORM_FULL(k_norm_bwd_ring, __nv_bfloat16, 8);
+    return s.vec == 4   ? JMIX_NORM_NARROW(k_norm_bwd_ring, __nv_bfloat16, 4)
+           : s.vec == 2 ? JMIX_NORM_NARROW(k_norm_bwd_ring, __nv_bfloat16, 2)
+                        : JMIX_NORM_NARROW(k_norm_bwd_ring, __nv_bfloat16, 1);
+  }
+  if (s.full) return JMIX_NORM_FULL(k_norm_bwd_ring, float, 4);
+  return s.vec == 2 ? JMIX_NORM_NARROW(k_norm_bwd_ring, float, 2)
+                    : JMIX_NORM_NARROW(k_norm_bwd_ring, float, 1);
 }
 
+NormKern<NormBwdArgs> bwd_kernel(const NormShape& s, jm_dtype io) {
+  if (io == JM_BF16)
+    return s.full ? JMIX_NORM_FULL(k_norm_bwd, __nv_bfloat16, 8)
+                  : JMIX_NORM_NARROW(k_norm_bwd, __nv_bfloat16, 1);
+  return s.full ? JMIX_NORM_FULL(k_norm_bwd, float, 4) : JMIX_NORM_NARROW(k_norm_bwd, float, 1);
+}
+#undef JMIX_NORM_FULL
+#undef JMIX_NORM_NARROW
+
 size_t ring_stage(int64_t cols, bool g_sum, const NormShape& s, jm_dtype io) {
-  return (size_t)ring_part_bytes((size_t)s.rpc * cols * (io == JM_BF16 ? 2 : 4), s.vec == 1) *
+  return (size_t)ring_part_bytes((size_t)s.rpc * cols * (io == JM_BF16 ? 2 : 4), !s.full) *
          (g_sum ? 3 : 2);
 }
 
 // Stages of the backward's ring (at least 2), or 0 where the loading kernel runs: rows of
-// x apart by no multiple of 16 bytes, or too long for two stages.  CTAs of 256 threads share
-// an SM in pairs.
+// x apart by no multiple of 16 bytes, or too long for two stages.
 int ring_stages(int64_t cols, int64_t x_stride, bool g_sum, const NormShape& s, jm_dtype io) {
-  if ((s.vec == 1 && x_stride != cols) || (s.vec > 1 && s.nv != 2)) return 0;
-  const size_t most = s.threads() <= 256 ? 110 * 1024 : 220 * 1024;
+  if ((!s.full && x_stride != cols) || (s.full && s.nv != 2)) return 0;
+  const size_t most = 220 * 1024 / s.ring_ctas();
   const int n = (int)(most / ring_stage(cols, g_sum, s, io));
   return n < 2 ? 0 : n < kNormMaxStages ? n : kNormMaxStages;
 }
@@ -649,7 +695,7 @@ size_t ring_bytes(int64_t cols, bool g_sum, int stages, const NormShape& s, jm_d
 // CTAs of the backward: as many as are resident at once, so that there are few
 // partial rows to add.
 int64_t bwd_ctas(int64_t rows, const NormShape& s, bool ring) {
-  const int64_t most = (int64_t)kNormSMs * (s.threads() > 256 ? 1 : ring ? 2 : 3);
+  const int64_t most = (int64_t)kNormSMs * (ring ? s.ring_ctas() : s.threads() > 256 ? 1 : 3);
   const int64_t need = (rows + s.rpc - 1) / s.rpc;
   return need < most ? need : most;
 }
@@ -657,12 +703,14 @@ int64_t bwd_ctas(int64_t rows, const NormShape& s, bool ring) {
 }  // namespace
 
 size_t norm_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t x_stride, jm_dtype io) {
-  const NormShape s = norm_shape(cols, x_stride, io);
-  return sizeof(ErrFlags) + align256((size_t)(bwd_ctas(rows, s, false) * s.rpc * 2 * cols) * 4);
+  // partial rows of whichever kernel leaves more (which one runs depends on g_sum too)
+  const NormShape r = norm_shape(cols, x_stride, io, true), s = norm_shape(cols, x_stride, io, false);
+  const int64_t ring = bwd_ctas(rows, r, true), plain = bwd_ctas(rows, s, false) * s.rpc;
+  return sizeof(ErrFlags) + align256((size_t)((ring > plain ? ring : plain) * 2 * cols) * 4);
 }
 
 cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p) {
-  const NormShape s = norm_shape(a.cols, a.x_stride, io);
+  const NormShape s = norm_shape(a.cols, a.x_stride, io, true);
   a.wpr = s.wpr;
   a.rpc = s.rpc;
   const int64_t ctas = (a.rows + s.rpc - 1) / s.rpc;
@@ -674,14 +722,15 @@ cudaError_t run_norm_fwd(NormFwdArgs a, jm_dtype io, Problem& p) {
 }
 
 cudaError_t run_norm_bwd(NormBwdArgs a, void* g_w, void* g_b, char* ws, jm_dtype io, Problem& p) {
-  const NormShape s = norm_shape(a.cols, a.x_stride, io);
+  NormShape s = norm_shape(a.cols, a.x_stride, io, true);
+  a.stages = ring_stages(a.cols, a.x_stride, a.g_sum != nullptr, s, io);
+  if (a.stages == 0) s = norm_shape(a.cols, a.x_stride, io, false);
   a.wpr = s.wpr;
   a.rpc = s.rpc;
   a.err = reinterpret_cast<ErrFlags*>(ws);
   const bool sums = g_w || g_b;
   float* part = reinterpret_cast<float*>(ws + sizeof(ErrFlags));
   a.part = sums ? part : nullptr;
-  a.stages = ring_stages(a.cols, a.x_stride, a.g_sum != nullptr, s, io);
   const int64_t ctas = bwd_ctas(a.rows, s, a.stages > 0);
   const int64_t part_rows = a.stages > 0 ? ctas : ctas * s.rpc;
   cudaError_t e = cudaSuccess;

@@ -258,3 +258,46 @@ def test_norm_on_another_stream_and_captured():
         torch.cuda.synchronize()
         d2, y2, s2, st2 = run_fwd(dict(t, x=x), "bf16", 1, residual=True, bias=True)
         assert torch.equal(y, y2) and torch.equal(s, s2) and torch.equal(st, st2)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("rows,cols", [(5000, 1), (2501, 3), (9999, 7), (20000, 131), (3001, 1021),
+                                       (1301, 943), (701, 4357), (401, 8191), (307, 16383),
+                                       (3000, 514), (2999, 2052)])
+def test_norm_of_many_ragged_rows(rows, cols, kind, io):
+    """Rows that are no multiple of 16 bytes, more than one round of the GPU's CTAs."""
+    t = make(rows, cols, io, seed=rows + cols)
+    d, s, st = check_fwd(t, io, kind, residual=True, bias=bool(kind))
+    check_bwd(t, io, kind, d, s, st, g_sum=True)
+    d, s, st = check_fwd(t, io, kind, residual=False, bias=False)
+    check_bwd(t, io, kind, d, s, st, g_sum=False, alias=True)
+
+
+@pytest.mark.parametrize("rows", [2000, 2007])
+def test_norm_of_ragged_rows_in_place_and_in_bounds(rows):
+    """y over x, sum over the residual, g_x over g_sum; the values around the tensors stay."""
+    import torch
+    from mamba_selective_scan_jamba_b200 import devio, jmix
+    cols = 1013
+    t = make(rows, cols, "bf16", seed=3)
+    d, y, s, st = run_fwd(t, "bf16", 1, residual=True, bias=True)
+    n = rows * cols
+
+    def guarded(v):
+        g = torch.full((n + 64,), 9.0, device="cuda", dtype=torch.bfloat16)
+        g[:n] = v.flatten()
+        return g, g[:n].view(rows, cols)
+    xg, x = guarded(t["x"])
+    rg, r = guarded(t["r"])
+    jmix.jm_norm_fwd(d, x, t["w"], x, bias=t["b"], residual=r, sum_out=r)
+    assert torch.equal(x, y) and torch.equal(r, s)
+    nb = jmix.jm_norm_bwd_workspace_size(d)
+    ws = devio.workspace(nb)
+    gx = torch.empty_like(y)
+    jmix.jm_norm_bwd(d, t["gy"], s, t["w"], st, gx, ws, nb, g_sum=t["gs"])
+    sg, over = guarded(t["gs"])
+    jmix.jm_norm_bwd(d, t["gy"], s, t["w"], st, over, ws, nb, g_sum=over)
+    assert torch.equal(over, gx)
+    for g in (xg, rg, sg):
+        assert (g[n:] == 9.0).all()
