@@ -222,20 +222,20 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 
-// Drain warps: counts `v` after all of their earlier writes.
+// Drain warps: counts `v` after all of their earlier writes (the barrier orders them before
+// the counting thread's release).
 __device__ __forceinline__ void epi_add(unsigned* p, unsigned v, int et) {
-  __threadfence();
   epi_sync();
   if (et == 0) add_release(p, v);
 }
 
-__device__ __forceinline__ bool epi_wait(unsigned* p, unsigned n, ErrFlags* err, unsigned site,
-                                         int et, int* flag) {
-  if (et == 0) *flag = wait_count(p, n, err, site) ? 1 : 0;
-  epi_sync();
-  const bool ok = *flag != 0;
-  epi_sync();
-  return ok;
+// One warp waits for a count.
+__device__ __forceinline__ bool warp_wait(unsigned* p, unsigned n, ErrFlags* err, unsigned site) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_count(p, n, err, site) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok != 0;
 }
 
 // ------------------------------------------------------------------- routing
@@ -474,64 +474,84 @@ __device__ void join_h(const MoeKArgs& a, const Entry& en, unsigned tile, unsign
   }
 }
 
-// out of every token: its experts' products weighted in the order of the choices.  A
-// thread takes U groups of 4 columns at a time, so that their loads are in flight together.
-template <int U>
-__device__ __forceinline__ void form_out(const MoeKArgs& a, const Lists& L, const Line& l) {
-  const unsigned d4 = (unsigned)a.D / 4, total = (unsigned)a.T * d4, step = gridDim.x * kThreads;
-  const int64_t width = (int64_t)l.tiles * 256;
-  for (unsigned i0 = blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += U * step) {
-    float4 o[U];
-    uint2 res[U];
-    unsigned t[U], d[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const unsigned i = min(i0 + u * step, total - 1);
-      t[u] = i / d4;
-      d[u] = (i - t[u] * d4) * 4;
-      res[u] = make_uint2(0u, 0u);
-      if (a.residual) res[u] = reinterpret_cast<const uint2*>(a.residual)[i];
-    }
-    for (int c = 0; c < a.topk; ++c) {
-      float4 v[U];
-      float w[U];
-      const float* next[U];
-      unsigned more[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const unsigned p = t[u] * a.topk + c;
-        const int r = L.row[p], ent = L.ent[r];
-        w[u] = a.wgt[p];
-        unsigned c0, c1;
-        l.ctas_of(ent * l.tiles + (d[u] >> 8), c0, c1);
-        const int64_t at = (int64_t)(r - L.entry[ent].r0) * 256 + (d[u] & 255);
-        v[u] = ld4(c0 == c1 ? a.y + r * width + d[u] : part_of(a, 1, c0, 1) + at);
-        next[u] = part_of(a, 1, c0 + 1, 0) + at;
-        more[u] = c1 - c0;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float* q = next[u];
+// out of every token: its experts' products weighted in the order of the choices, by
+// groups of 4 columns.
+struct OutGroup {
+  unsigned t, d;   // token, first column
+  uint2 res;
+  float4 sum;
+  __device__ __forceinline__ void start(const MoeKArgs& a, unsigned i) {
+    const unsigned d4 = (unsigned)a.D / 4;
+    t = i / d4;
+    d = (i - t * d4) * 4;
+    res = make_uint2(0u, 0u);
+    if (a.residual) res = reinterpret_cast<const uint2*>(a.residual)[i];
+    sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  template <typename W>
+  __device__ __forceinline__ void add(const W& term, const float4& v) {
+    sum.x = fmaf(term.w, v.x, sum.x);
+    sum.y = fmaf(term.w, v.y, sum.y);
+    sum.z = fmaf(term.w, v.z, sum.z);
+    sum.w = fmaf(term.w, v.w, sum.w);
+  }
+  __device__ __forceinline__ void store(const MoeKArgs& a, unsigned i) const {
+    reinterpret_cast<uint2*>(a.out)[i] =
+        make_uint2(pack2(sum.x + __uint_as_float(res.x << 16),
+                         sum.y + __uint_as_float(res.x & 0xffff0000u)),
+                   pack2(sum.z + __uint_as_float(res.y << 16),
+                         sum.w + __uint_as_float(res.y & 0xffff0000u)));
+  }
+};
+
+// The product of a group with its token's c-th expert: in y, or in partial tiles.
+struct Term {
+  const float* p;
+  const float* next;
+  unsigned more;
+  float w;
+  __device__ __forceinline__ void find(const MoeKArgs& a, const Lists& L, const Line& l,
+                                       const OutGroup& o, int c) {
+    const unsigned pair = o.t * a.topk + c;
+    const int r = L.row[pair], ent = L.ent[r];
+    w = a.wgt[pair];
+    unsigned c0, c1;
+    l.ctas_of(ent * l.tiles + (o.d >> 8), c0, c1);
+    const int64_t at = (int64_t)(r - L.entry[ent].r0) * 256 + (o.d & 255);
+    p = c0 == c1 ? a.y + r * (int64_t)l.tiles * 256 + o.d : part_of(a, 1, c0, 1) + at;
+    next = part_of(a, 1, c0 + 1, 0) + at;
+    more = c1 - c0;
+  }
+  __device__ __forceinline__ float4 first() const { return ld4(p); }
+  __device__ __forceinline__ float4 rest(float4 v, const MoeKArgs& a) const {
 #pragma unroll 8
-        for (unsigned k = 0; k < more[u]; ++k) add4(v[u], ld4(q + (int64_t)k * a.NB * 512));
-        o[u].x = fmaf(w[u], v[u].x, o[u].x);
-        o[u].y = fmaf(w[u], v[u].y, o[u].y);
-        o[u].z = fmaf(w[u], v[u].z, o[u].z);
-        o[u].w = fmaf(w[u], v[u].w, o[u].w);
+    for (unsigned k = 0; k < more; ++k) add4(v, ld4(next + (int64_t)k * a.NB * 512));
+    return v;
+  }
+};
+
+// Four groups a thread at a time, so that their loads are in flight together.
+__device__ __forceinline__ void form_out(const MoeKArgs& a, const Lists& L, const Line& l) {
+  constexpr int U = 4;
+  const unsigned total = (unsigned)a.T * (a.D / 4), step = gridDim.x * kThreads;
+  for (unsigned i0 = blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += U * step) {
+    OutGroup o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) o[u].start(a, min(i0 + u * step, total - 1));
+    for (int c = 0; c < a.topk; ++c) {
+      Term term[U];
+      float4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        term[u].find(a, L, l, o[u], c);
+        v[u] = term[u].first();
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) o[u].add(term[u], term[u].rest(v[u], a));
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned i = i0 + u * step;
-      if (i >= total) break;
-      const uint2 q = res[u];
-      reinterpret_cast<uint2*>(a.out)[i] =
-          make_uint2(pack2(o[u].x + __uint_as_float(q.x << 16),
-                           o[u].y + __uint_as_float(q.x & 0xffff0000u)),
-                     pack2(o[u].z + __uint_as_float(q.y << 16),
-                           o[u].w + __uint_as_float(q.y & 0xffff0000u)));
-    }
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * step < total) o[u].store(a, i0 + u * step);
   }
 }
 
@@ -547,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int stage_bytes = kWBytes + a.NB * 128;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int epi_flag;
+  __shared__ int out_flag;
   __shared__ int4 gather_rows[32];   // token rows of the block, 4 a gather
   Lists& L = *reinterpret_cast<Lists*>(smem + S * stage_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -634,14 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           tok[min(r + 2, last)], tok[min(r + 3, last)]);
             __syncwarp();
           } else {
-            int there = 1;
-            if (lane == 0)
-              there = wait_count(&a.sync->ready[w.ent], line[0].tiles * line[0].ksteps, a.err, 93);
-            if (__shfl_sync(0xffffffffu, there, 0) == 0) {
-              ok = false;
-              break;
-            }
-            __syncwarp();
+            ok = warp_wait(&a.sync->ready[w.ent], line[0].tiles * line[0].ksteps, a.err, 93);
+            if (!ok) break;
             fence_proxy_async_global();
           }
         }
@@ -761,7 +775,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // What others wait for is counted once, behind one fence: a fence after each unit
         // held the drain up for 2 us of every 4 with units of 3 steps.
         fence_proxy_async_global();   // h is read by TMA
-        __threadfence();
         ok = epi_all(ok);
         // The cut units this CTA took part in are its first and its last.
         unsigned cut_u[2], cut_steps[2], block = ~0u, done = 0;
@@ -788,29 +801,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i < cuts; ++i) {
           unsigned c0, c1;
           l.ctas_of(cut_u[i], c0, c1);
-          ok = epi_wait(&a.sync->unit[c0], l.ksteps, a.err, 98, et, &epi_flag);
+          ok = warp_wait(&a.sync->unit[c0], l.ksteps, a.err, 98);
           const unsigned ent = cut_u[i] / l.tiles;
           if (ok) join_h(a, L.entry[ent], cut_u[i] - ent * l.tiles, c0, c1, et);
         }
-        if (ok && cuts) {
+        if (cuts) {
           fence_proxy_async_global();
-          __threadfence();
-          epi_sync();
-          for (int i = 0; et == 0 && i < cuts; ++i)
+          ok = epi_all(ok);
+          for (int i = 0; ok && et == 0 && i < cuts; ++i)
             add_release(&a.sync->ready[cut_u[i] / l.tiles], cut_steps[i]);
         }
       }
     }
     epi_add(&a.sync->done, 1, et);
-    epi_wait(&a.sync->done, gridDim.x, a.err, 99, et, &epi_flag);
   }
+  // The last sum.  Where a thread has one group of columns at most, what it needs for the
+  // first two experts is looked up before the wait.
+  const unsigned groups = (unsigned)a.T * (a.D / 4), mine = blockIdx.x * kThreads + tid;
+  const bool few = groups <= gridDim.x * kThreads, has = few && mine < groups;
+  OutGroup o;
+  Term term[2];
+  if (has) {
+    o.start(a, mine);
+    term[0].find(a, L, line[1], o, 0);
+    if (a.topk > 1) term[1].find(a, L, line[1], o, 1);
+  }
+  if (tid == 64)
+    out_flag = wait_count(&a.sync->done, gridDim.x, a.err, 99) ? 1 : 0;
   tc_fence_before();
   __syncthreads();
-  if (epi_flag) {
-    if ((unsigned)a.T * a.D / 4 <= gridDim.x * kThreads)
-      form_out<1>(a, L, line[1]);
-    else
-      form_out<4>(a, L, line[1]);
+  if (out_flag) {
+    if (has) {
+      float4 v[2];
+      v[0] = term[0].first();
+      if (a.topk > 1) v[1] = term[1].first();
+      o.add(term[0], term[0].rest(v[0], a));
+      if (a.topk > 1) o.add(term[1], term[1].rest(v[1], a));
+      for (int c = 2; c < a.topk; ++c) {
+        term[0].find(a, L, line[1], o, c);
+        o.add(term[0], term[0].rest(term[0].first(), a));
+      }
+      o.store(a, mine);
+    } else if (!few) {
+      form_out(a, L, line[1]);
+    }
   }
   if (warp == 1) {
     tc_fence_after();
