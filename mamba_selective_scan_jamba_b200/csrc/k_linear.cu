@@ -68,6 +68,10 @@ struct PairArgs {
   ErrFlags* err;
   bool single;     // no CTA has two tiles
   bool clear_err;  // the first kernel of a call clears the error header
+  // The kernel before this one writes nothing that this one reads or writes, and has itself
+  // waited for all that came before: its end is waited for at this kernel's end, so that the
+  // two overlap.
+  bool late_wait;
 };
 
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();   // both CTAs' barriers exist before either signals the other's
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  grid_dep_wait();
+  if (!g.late_wait) grid_dep_wait();
   grid_dep_launch();
   // (a wait gives up after 2 s: no CTA can have recorded one yet)
   if (g.clear_err && blockIdx.x == 0 && threadIdx.x < sizeof(ErrFlags) / 4)
@@ -484,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       d.close();
     }
   }
+  if (g.late_wait) grid_dep_wait();
   tc_fence_before();
   cluster_sync();   // no CTA leaves while another may still signal it or read its tile
   if (warp == 1) {
@@ -709,9 +714,10 @@ cudaError_t launch_pair(const CUtensorMap (&tm)[5], const PairArgs& g, cudaStrea
 }
 
 // C[M, N] = A . B^T with the epilogue `ep`.  AMN / BMN: A is stored [K, M], B [K, N].
+// `apart`: see late_wait.
 template <bool AMN, bool BMN>
 cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* B,
-                    const Epilogue& ep, float* part, ErrFlags* err, bool clear_err, Problem& p) {
+                    const Epilogue& ep, float* part, ErrFlags* err, bool clear_err, bool apart, Problem& p) {
   const Cut c = choose_cut(M, N, K);
   CUtensorMap tm[5];
   bool ok = (AMN ? bf16_map(&tm[0], A, K, M, 64) : bf16_map(&tm[0], A, M, K, kHalf)) &&
@@ -734,6 +740,7 @@ cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* 
   g.err = err;
   g.single = (int64_t)g.m_tiles * g.n_tiles * g.splits <= kPairs || c.cpairs > 1;
   g.clear_err = clear_err;
+  g.late_wait = apart && !clear_err && c.splits == 1;   // (the partial tiles' place is shared)
   cudaError_t e = c.bn == 256 ? launch_pair<AMN, BMN, 256>(tm, g, p.stream)
                               : launch_pair<AMN, BMN, 128>(tm, g, p.stream);
   if (e != cudaSuccess) return e;
@@ -804,9 +811,9 @@ cudaError_t run_linear_fwd(const LinearArgs& a, Problem& p) {
   ep.act = a.act;
   launches_begin(p);
   if (linear_few(a.M))
-    return run_linear_few(a.M, a.N, a.K, a.x, a.w, false, ep, err, true, p);
+    return run_linear_few(a.M, a.N, a.K, a.x, a.w, false, ep, err, true, false, p);
   return product<false, false>(a.M, a.N, a.K, a.x, a.w, ep,
-                               reinterpret_cast<float*>(a.ws + sizeof(ErrFlags)), err, true, p);
+                               reinterpret_cast<float*>(a.ws + sizeof(ErrFlags)), err, true, false, p);
 }
 
 cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
@@ -847,14 +854,17 @@ cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
   ep.act = JM_ACT_NONE;
   if (a.g_x) {  // [M, K] = g_p [M, N] . w [N, K]
     ep.out = static_cast<__nv_bfloat16*>(a.g_x);
-    e = linear_few(a.M) ? run_linear_few(a.M, a.K, a.N, gp, a.w, true, ep, err, clear, p)
-                        : product<false, true>(a.M, a.K, a.N, gp, a.w, ep, w.part, err, clear, p);
+    // (apart from the bias's sums where these came last)
+    e = linear_few(a.M)
+            ? run_linear_few(a.M, a.K, a.N, gp, a.w, true, ep, err, clear, a.g_bias != nullptr, p)
+            : product<false, true>(a.M, a.K, a.N, gp, a.w, ep, w.part, err, clear,
+                                   a.g_bias != nullptr, p);
     if (e != cudaSuccess) return e;
   }
   if (a.g_w) {  // [N, K] = g_p [M, N]^T . x [M, K]
     ep.out = static_cast<__nv_bfloat16*>(a.g_w);
     e = product<true, true>(a.N, a.K, a.M, gp, a.x, ep, w.part, err, clear && !a.g_x,
-                            p);
+                            a.g_x || a.g_bias, p);
   }
   return e;
 }

@@ -40,6 +40,7 @@ struct FewArgs {
   Epilogue ep;
   ErrFlags* err;
   bool clear_err;
+  bool late_wait;   // wait for the kernel before this one at the end
 };
 
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot, base = smem_u32(smem);
-  grid_dep_wait();
+  if (!g.late_wait) grid_dep_wait();
   grid_dep_launch();
   // (a wait gives up after 2 s: no CTA can have recorded one yet)
   if (g.clear_err && blockIdx.x == 0 && tid < (int)(sizeof(ErrFlags) / 4))
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     finish8(g.ep, v, (int64_t)t * g.N + col, col);
   }
+  if (g.late_wait) grid_dep_wait();
   cluster_sync();   // no CTA leaves while another may read its tile
   if (warp == 1) {
     tc_fence_after();
@@ -301,7 +303,7 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& x, const FewArgs
 bool linear_few(int64_t M) { return M <= kFewRows; }
 
 cudaError_t run_linear_few(int64_t T, int64_t N, int64_t K, const void* x, const void* w, bool w_mn,
-                           const Epilogue& ep, ErrFlags* err, bool clear_err, Problem& p) {
+                           const Epilogue& ep, ErrFlags* err, bool clear_err, bool apart, Problem& p) {
   const FewShape f = few_shape(T, N, K);
   FewArgs g{};
   g.T = (int)T;
@@ -314,6 +316,7 @@ cudaError_t run_linear_few(int64_t T, int64_t N, int64_t K, const void* x, const
   g.ep = ep;
   g.err = err;
   g.clear_err = clear_err;
+  g.late_wait = apart && !clear_err;
   CUtensorMap tw, tx;
   if (!(w_mn ? map(&tw, w, K, N, 64, 3) : map(&tw, w, N, K, kTile, 3)) ||
       !map(&tx, x, T, K, f.nb, 2))
