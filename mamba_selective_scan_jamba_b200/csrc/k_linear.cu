@@ -164,11 +164,21 @@ struct Drain {
   uint32_t res_parity = 0;
   int buf = 0;
   bool ok = true;
+  __nv_bfloat16* bias;   // shared: of the tile's two chunks, loaded before its accumulator
+                         // is waited for
 
-  __device__ __forceinline__ Drain(const PairArgs& g, uint8_t* stage, uint32_t res_bar, int grp,
-                                   int r)
+  __device__ __forceinline__ Drain(const PairArgs& g, uint8_t* stage, __nv_bfloat16* bias,
+                                   uint32_t res_bar, int grp, int r)
       : g(g), stage(stage), sw(r & 7), grp(grp), res_bar(res_bar), row_at(r * 128),
-        first(r == 0) {}
+        first(r == 0), bias(bias) {}
+
+  // The bias of 64 columns from `col` and of 64 from col + 128, in the tile's half `at` of the
+  // place (the group's next barrier is before their use).
+  __device__ __forceinline__ void load_bias(int at, int64_t col) const {
+    const int r = row_at / 128;
+    const int64_t c = col + (r >> 6) * 128 + (r & 63);
+    if (g.ep.bias) bias[at * 128 + r] = c < g.N ? g.ep.bias[c] : __float2bfloat16_rn(0.0f);
+  }
   __device__ __forceinline__ uint4* mine(int b) const {
     return reinterpret_cast<uint4*>(stage + b * kOutBytes + row_at);
   }
@@ -207,17 +217,15 @@ struct Drain {
   }
 
   __device__ __forceinline__ void finish(const CUtensorMap& tm_out, const CUtensorMap& tm_pre,
-                                         uint32_t (&v)[64], int64_t col, int64_t row0) {
+                                         uint32_t (&v)[64], int64_t col, int64_t row0, int chunk) {
     if (g.ep.bias) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (col + 8 * i < g.N) {
-          float bv[8];
-          unpack8(__ldg(reinterpret_cast<const uint4*>(g.ep.bias + col) + i), bv);
+        float bv[8];
+        unpack8(reinterpret_cast<const uint4*>(bias + chunk * 64)[i], bv);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            v[8 * i + k] = __float_as_uint(__uint_as_float(v[8 * i + k]) + bv[k]);
-        }
+        for (int k = 0; k < 8; ++k)
+          v[8 * i + k] = __float_as_uint(__uint_as_float(v[8 * i + k]) + bv[k]);
       }
     }
     if (g.ep.pre) {
@@ -271,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kStage = stage_bytes(BN), kBHalf = BN / 2;
   const int S = stages(BN, g.single);
   extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) __nv_bfloat16 bias_of[2][256];   // [group][tile parity][chunk][64]
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   // (behind the float32 tile that a cluster's pairs exchange)
   uint8_t* staging = g.single ? smem + (g.cpairs > 1 ? BN * kHalf * 4 : 0) : smem + S * kStage;
@@ -363,6 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       Place acc(2);
       bool ok = true;
       const uint32_t base = smem_u32(smem);
+      const uint64_t ad_base = AMN ? sw128_mnmajor_desc(base, 8192) : sw128_kmajor_desc(base);
+      const uint64_t bd_base = BMN ? sw128_mnmajor_desc(base + kABytes, 8192)
+                                   : sw128_kmajor_desc(base + kABytes);
       for (unsigned w = pair; ok && w < items; w += npairs, acc.next()) {
         const Item q = item_of(g, w, kchunks);
         const int b = acc.s;
@@ -376,15 +388,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t ab = base + (uint32_t)(s * kStage), bb = ab + kABytes;
+          // descriptors by addition: the start address is their low 14 bits, in 16 bytes
+          const uint64_t ad0 = ad_base + (uint64_t)(s * (kStage / 16));
+          const uint64_t bd0 = bd_base + (uint64_t)(s * (kStage / 16));
 #pragma unroll
-          for (int kk = 0; kk < kK / 16; ++kk) {
-            const uint64_t ad = AMN ? sw128_mnmajor_desc(ab + kk * 2048, 8192)
-                                    : sw128_kmajor_desc(ab + kk * 32);
-            const uint64_t bd = BMN ? sw128_mnmajor_desc(bb + kk * 2048, 8192)
-                                    : sw128_kmajor_desc(bb + kk * 32);
-            umma_f16_pair(d_tmem, ad, bd, idesc, (kc > q.k0 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < kK / 16; ++kk)
+            umma_f16_pair(d_tmem, ad0 + kk * (AMN ? 128 : 2), bd0 + kk * (BMN ? 128 : 2), idesc,
+                          (kc > q.k0 || kk > 0) ? 1u : 0u);
           umma_commit_pair(smem_u32(&empty[s]), both);
         }
         if (ok) umma_commit_pair(smem_u32(&acc_full[b]), both);
@@ -397,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool split = g.splits > 1;
     const int cw = split ? 32 : 64;                   // columns in 128 bytes
     const uint32_t acc_empty_leader = cluster_addr(smem_u32(&acc_empty[0]), crank & ~1u);
-    Drain d(g, staging + grp * 2 * kOutBytes, smem_u32(&res_full[grp]), grp, r);
+    Drain d(g, staging + grp * 2 * kOutBytes, bias_of[grp], smem_u32(&res_full[grp]), grp, r);
     Place acc(2);
     // (a thread whose wait ran out goes on without waiting, so that its group's barriers
     // stay matched; the error header says that the values are not to be used)
@@ -428,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         break;   // one tile per cluster; it is finished below
       }
+      if (!split) d.load_bias(b, n0 + grp * 64);
       for (int c = grp * cw; rows && c < BN && n0 + c < g.N; c += 2 * cw) {
         const int64_t col = n0 + c;
         if (!g.single) d.open(tm_res, col, row0);
@@ -445,14 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16(tbase + c + 32, *reinterpret_cast<uint32_t(*)[16]>(v + 32));
           tmem_ld16(tbase + c + 48, *reinterpret_cast<uint32_t(*)[16]>(v + 48));
           tmem_ld_wait();
-          d.finish(tm_out, tm_pre, v, col, row0);
+          d.finish(tm_out, tm_pre, v, col, row0, 2 * b + (c >> 7));
         }
       }
       // the accumulator is free once it is complete and this warp has read its part
       if (!waited) d.ok = d.ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_empty_leader + (uint32_t)(b * 8));
+      if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + (uint32_t)(b * 8));
     }
     if (g.cpairs == 1) d.close();
   }
@@ -461,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();   // the cluster's tiles are all there
     if (warp >= 2) {
       const int grp = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;
-      Drain d(g, staging + grp * 2 * kOutBytes, smem_u32(&res_full[grp]), grp, r);
+      Drain d(g, staging + grp * 2 * kOutBytes, bias_of[grp], smem_u32(&res_full[grp]), grp, r);
       const Item q = item_of(g, pair, kchunks);
       const int64_t row0 = (int64_t)q.mt * (2 * kHalf) + rank * kHalf;
       // this pair's columns: BN / cpairs of them, 64 at a time
@@ -469,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = c0 + grp * 64; c < c0 + cols; c += 128) {
         const int64_t col = (int64_t)q.nt * BN + c;
         if (row0 >= g.M || col >= g.N) break;
+        d.load_bias(0, col);
         d.open(tm_res, col, row0);
         uint32_t v[64];
         const uint32_t at = smem_u32(smem) + (uint32_t)((c / 4) * kHalf + r) * 16;
@@ -483,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[4 * i + k] = __float_as_uint(p ? __uint_as_float(v[4 * i + k]) + o[k] : o[k]);
           }
         }
-        d.finish(tm_out, tm_pre, v, col, row0);
+        d.finish(tm_out, tm_pre, v, col, row0, 0);
       }
       d.close();
     }

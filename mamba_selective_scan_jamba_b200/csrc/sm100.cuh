@@ -278,6 +278,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same without ordering the thread's memory accesses: for handing TMEM back, whose loads
+// have completed (tcgen05.wait::ld, tcgen05.fence).  The release at cluster scope waits for
+// every store in flight, 2000 cycles behind an epilogue's.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 // 2-D tile load into this CTA's shared memory whose completion is counted on
 // the LEADER's barrier at offset `bar` (cta_group::2).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map,
