@@ -92,12 +92,14 @@ struct MoeKArgs {
   ErrFlags* err;
 };
 
-// A phase's line of work: `parts` parts of `quant` steps, cut between `ctas` CTAs.
+// A phase's line of work: units of `ksteps` steps in `ppu` parts of `quant` steps (the last
+// one may have fewer), the parts cut between `ctas` CTAs.
 struct Line {
-  unsigned tiles, ksteps, total, quant, parts, ctas;
+  unsigned tiles, ksteps, total, quant, ppu, parts, ctas;
   double inv;   // 1 / parts
   __device__ __forceinline__ unsigned start(unsigned c) const {
-    return (unsigned)((uint64_t)parts * min(c, ctas) / ctas) * quant;
+    const unsigned p = (unsigned)((uint64_t)parts * min(c, ctas) / ctas), u = p / ppu;
+    return u * ksteps + (p - u * ppu) * quant;
   }
   // the CTA whose range holds the part p: ((p + 1) ctas - 1) / parts (below 2^32, checked
   // on the host; by a multiplication, which may be one off)
@@ -111,24 +113,21 @@ struct Line {
   }
   // the first and the last CTA of a unit
   __device__ __forceinline__ void ctas_of(unsigned unit, unsigned& c0, unsigned& c1) const {
-    if (quant > 1) {   // whole units
-      c0 = c1 = cta_of_part(unit);
-    } else {
-      c0 = cta_of_part(unit * ksteps);
-      c1 = cta_of_part((unit + 1) * ksteps - 1);
-    }
+    c0 = cta_of_part(unit * ppu);
+    c1 = ppu == 1 ? c0 : cta_of_part((unit + 1) * ppu - 1);
   }
 };
 
-// Whole units or ranges cut anywhere?  Cut ranges give every CTA the same bytes, but
-// their partial tiles cost `join_us`.  Whole units leave the last round's CTAs to
-// themselves, and one SM's loads from HBM reach about 60 GB/s: a step of 32 KB takes the
-// whole GPU 5 ns, but one SM 550 ns.  Measured: one token, 2 of 16 experts of 4096 x 14336
-// (224 units of 64 steps), cut 128 us, whole 136 us; 13 tokens, 8 experts of 512 x 1416
-// (96 units of 8 steps), cut 34 us, whole 27 us.  There are no more CTAs than parts, so
-// that no range between two others is empty.
+// Whole units or cut ones?  Cut ranges give every CTA the same bytes, but their partial
+// tiles cost `join_us`.  Whole units leave the last round's CTAs to themselves, and one SM's
+// loads from HBM reach about 60 GB/s: a step of 32 KB takes the whole GPU 5 ns, but one SM
+// 550 ns.  Measured: one token, 2 of 16 experts of 4096 x 14336 (224 units of 64 steps), cut
+// 128 us, whole 136 us; 13 tokens, 8 experts of 512 x 1416 (96 units of 8 steps), cut 34 us,
+// whole 27 us.  Where ranges are short a unit is cut into at most `most` parts, since
+// somebody has to add them all (2 units of 64 steps cut into single ones: 35 us).  There are
+// no more CTAs than parts, so that no range between two others is empty.
 __device__ __forceinline__ Line make_line(unsigned entries, unsigned rows, unsigned kdim,
-                                          unsigned tile_rows, float join_us) {
+                                          unsigned tile_rows, float join_us, unsigned most) {
   Line l;
   l.tiles = (rows + tile_rows - 1) / tile_rows;
   l.ksteps = (kdim + kK - 1) / kK;
@@ -138,9 +137,14 @@ __device__ __forceinline__ Line make_line(unsigned entries, unsigned rows, unsig
   const float all = (float)(rounds * gridDim.x * l.ksteps) * 0.005f, k = (float)l.ksteps;
   const float whole = fmaxf(all, (float)(rounds * l.ksteps) * 0.55f) +
                       (rest ? fmaxf((float)rest * k * 0.005f, k * 0.55f) : 0.0f);
-  const float cut = fmaxf((float)l.total * 0.005f, (float)l.total / (float)gridDim.x * 0.55f);
-  l.quant = whole <= cut + join_us ? l.ksteps : 1u;
-  l.parts = l.total / l.quant;
+  const unsigned least = (l.ksteps + most - 1) / most;   // steps of a part
+  const float cut = fmaxf((float)l.total * 0.005f,
+                          fmaxf((float)l.total / (float)gridDim.x, (float)least) * 0.55f);
+  l.quant = whole <= cut + join_us          ? l.ksteps
+            : l.total >= least * gridDim.x  ? 1u     // ranges of `least` steps by themselves
+                                            : least;
+  l.ppu = (l.ksteps + l.quant - 1) / l.quant;
+  l.parts = units * l.ppu;
   l.ctas = max(min(gridDim.x, l.parts), 1u);
   l.inv = 1.0 / (double)max(l.parts, 1u);
   return l;
@@ -454,7 +458,7 @@ __device__ void join_h(const MoeKArgs& a, const Entry& en, unsigned tile, unsign
       g[q] = ld4(p);
       u[q] = ld4(p + 128);
     }
-#pragma unroll 2
+#pragma unroll 4
     for (unsigned c = c0 + 1; c <= c1; ++c) {
 #pragma unroll
       for (int q = 0; q < U; ++q) {
@@ -600,10 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  // (partial tiles cost the first phase a round of counting and of h, 5 us; the second
+  // (partial tiles cost the first phase a round of counting and of h, 4 us; the second
   // sums them where it has to wait anyway)
-  const Line line[2] = {make_line(L.n_entries, a.F, a.D, 128, 5.0f),
-                        make_line(L.n_entries, a.D, a.F, 256, 1.0f)};
+  const Line line[2] = {make_line(L.n_entries, a.F, a.D, 128, 4.0f, 8),
+                        make_line(L.n_entries, a.D, a.F, 256, 1.0f, 16)};
 
   if (warp == 0) {
     if (elect_one()) {
