@@ -675,9 +675,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t fb = smem_u32(&full[p.s]), dst = base + p.s * stage_bytes;
             mbar_arrive_expect_tx(fb, (uint32_t)(n16 * 16 * 128));
             if (ph == 0) {
-              for (int q = 0; q < n16 * 4; ++q) {   // 4 rows by index at a time
-                const int4 t = gather_rows[q];
+#pragma unroll 2
+              for (int q = 0; q < n16 * 4; q += 2) {   // 4 rows by index at a time
+                const int4 t = gather_rows[q], u = gather_rows[q + 1];
                 tma_gather4(dst + q * 512, &tm_x, fb, k, t.x, t.y, t.z, t.w);
+                tma_gather4(dst + q * 512 + 512, &tm_x, fb, k, u.x, u.y, u.z, u.w);
               }
             } else {
               for (int q = 0; q < n16; ++q) tma_load_2d(dst + q * 2048, &tm_h, fb, k, en.r0 + q * 16);
@@ -756,11 +758,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ph == 0 && whole) {
             if (f < (unsigned)a.F) {
               __nv_bfloat16* hp = a.h + (int64_t)(en.r0 + c) * a.F + f;
+              // (all 16 first, so that they overlap; rows behind the last are not stored)
+              __nv_bfloat16 hv[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (c + i < en.n)
-                  hp[(int64_t)i * a.F] =
-                      __float2bfloat16_rn(glu(__uint_as_float(g[i]), __uint_as_float(q[i])));
+                hv[i] = __float2bfloat16_rn(glu(__uint_as_float(g[i]), __uint_as_float(q[i])));
+              const int n = en.n - c;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                if (i < n) *hp = hv[i];
+                hp += a.F;
+              }
             }
           } else {
 #pragma unroll
