@@ -531,40 +531,53 @@ __global__ void __launch_bounds__(256)
 }
 
 // g_p = g_out act'(pre) in bf16 (the operand of both products) and, for g_bias, its
-// column sums (unrounded, float32) over this CTA's rows.  A CTA takes 2048 columns
-// (8 per thread) x `rows` rows; one read of g_out and pre, one write of g_p.
-constexpr int kGpCols = 2048;
+// column sums (unrounded, float32) over this CTA's rows.  A CTA takes 8 tx columns (8 per
+// thread) x `rows` rows, 256 / tx of them at a time, so that a narrow matrix keeps its
+// threads busy too; one read of g_out and pre, one write of g_p.
+constexpr int kGpThreads = 256;
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kGpThreads)
     k_linear_gpre(const __nv_bfloat16* __restrict__ g_out, const __nv_bfloat16* __restrict__ pre,
-                  int act, int64_t M, int64_t N, int rows, __nv_bfloat16* __restrict__ gp,
+                  int act, int64_t M, int64_t N, int tx, int rows, __nv_bfloat16* __restrict__ gp,
                   float* __restrict__ part, ErrFlags* err) {
+  __shared__ float sums[kGpThreads * 8];   // [256 / tx][8 tx]
   grid_dep_wait();
   grid_dep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < sizeof(ErrFlags) / 4)
     reinterpret_cast<unsigned*>(err)[threadIdx.x] = 0u;
-  const int64_t col = (int64_t)blockIdx.x * kGpCols + threadIdx.x * 8;
-  if (col >= N) return;
+  const int x = threadIdx.x & (tx - 1), y = threadIdx.x / tx, step = kGpThreads / tx;
+  const int64_t col0 = (int64_t)blockIdx.x * tx * 8, col = col0 + x * 8;
   const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = min(M, r0 + rows);
   float sum[8] = {};
+  if (col < N) {
 #pragma unroll 4
-  for (int64_t r = r0; r < r1; ++r) {
-    float g[8];
-    unpack8(*reinterpret_cast<const uint4*>(g_out + r * N + col), g);
-    if (pre) {
-      float p[8];
-      unpack8(*reinterpret_cast<const uint4*>(pre + r * N + col), p);
+    for (int64_t r = r0 + y; r < r1; r += step) {
+      float g[8];
+      unpack8(*reinterpret_cast<const uint4*>(g_out + r * N + col), g);
+      if (pre) {
+        float p[8];
+        unpack8(*reinterpret_cast<const uint4*>(pre + r * N + col), p);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] *= act_grad(p[j], act);
-      *reinterpret_cast<uint4*>(gp + r * N + col) = pack8(g);
+        for (int j = 0; j < 8; ++j) g[j] *= act_grad(p[j], act);
+        *reinterpret_cast<uint4*>(gp + r * N + col) = pack8(g);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += g[j];
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += g[j];
   }
-  if (part) {
-    float4* d = reinterpret_cast<float4*>(part + (int64_t)blockIdx.y * N + col);
+  if (!part) return;
+  float4* d = reinterpret_cast<float4*>(step > 1 ? sums + threadIdx.x * 8
+                                                 : part + (int64_t)blockIdx.y * N + col);
+  if (step > 1 || col < N) {
     d[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
     d[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+  }
+  if (step == 1) return;   // (uniform in the CTA)
+  __syncthreads();
+  for (int c = threadIdx.x; c < tx * 8 && col0 + c < N; c += kGpThreads) {
+    float acc = 0.0f;
+    for (int q = 0; q < step; ++q) acc += sums[q * tx * 8 + c];
+    part[(int64_t)blockIdx.y * N + col0 + c] = acc;
   }
 }
 
@@ -578,6 +591,7 @@ __global__ void __launch_bounds__(512)
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float acc = 0.0f;
   if (c < N)
+#pragma unroll 4
     for (int64_t r = threadIdx.y; r < rows; r += 16) acc += part[r * N + c];
   sh[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
@@ -767,11 +781,19 @@ cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* 
   return e;
 }
 
-// Rows a CTA of k_linear_gpre takes: enough CTAs for the GPU, at most 64 rows each.
+// Threads of a CTA of k_linear_gpre along the columns (a power of two), and rows a CTA
+// takes: enough CTAs for the GPU, at least 4 rows a thread.
+int gpre_tx(int64_t N) {
+  int tx = 8;
+  while (tx < kGpThreads && tx * 8 < N) tx *= 2;
+  return tx;
+}
+
 int gpre_rows(int64_t M, int64_t N) {
-  const int64_t col_ctas = (N + kGpCols - 1) / kGpCols;
+  const int tx = gpre_tx(N);
+  const int64_t col_ctas = (N + tx * 8 - 1) / (tx * 8), least = 4 * (kGpThreads / tx);
   int64_t r = (M * col_ctas + 148 * 8 - 1) / (148 * 8);
-  r = r < 4 ? 4 : r;
+  r = r < least ? least : r;
   if (r < (M + 65534) / 65535) r = (M + 65534) / 65535;   // grid y limit
   return (int)r;
 }
@@ -843,10 +865,11 @@ cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
   const bool grad = a.act != JM_ACT_NONE && (a.g_x || a.g_w || a.g_bias);
   if (grad || a.g_bias) {
     const int rows = gpre_rows(a.M, a.N);
-    const dim3 grid((unsigned)((a.N + kGpCols - 1) / kGpCols), (unsigned)((a.M + rows - 1) / rows));
-    e = launch(k_linear_gpre, grid, dim3(256), 0, 1, p.stream,
+    const int tx = gpre_tx(a.N);
+    const dim3 grid((unsigned)((a.N + tx * 8 - 1) / (tx * 8)), (unsigned)((a.M + rows - 1) / rows));
+    e = launch(k_linear_gpre, grid, dim3(kGpThreads), 0, 1, p.stream,
                static_cast<const __nv_bfloat16*>(a.g_out),
-               grad ? static_cast<const __nv_bfloat16*>(a.pre) : nullptr, a.act, a.M, a.N, rows,
+               grad ? static_cast<const __nv_bfloat16*>(a.pre) : nullptr, a.act, a.M, a.N, tx, rows,
                w.gp, a.g_bias ? w.bias_part : nullptr, err);
     if (e != cudaSuccess) return e;
     launched(p, "k_linear_gpre");
