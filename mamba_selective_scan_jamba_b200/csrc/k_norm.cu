@@ -436,7 +436,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
   for (int64_t it = 0; it < rounds; ++it) {
     const int64_t row = first + it * step + group;
     const bool live = row < a.rows;
-    const float mean = st.x, rs = st.y;
+    // (a group without a row adds zeros whatever its last row's statistics were)
+    const float mean = live ? st.x : 0.0f, rs = live ? st.y : 0.0f;
     if (row + step < a.rows) st = stats[row + step];
     ok = ok && sm100::mbar_wait(sm100::smem_u32(&full[s]), parity, a.err, 111);
     uint8_t* stage = ring + s * stage_bytes;
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
       unpack<T, VEC>(rw[v], w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        xh[v][j] = in ? (xh[v][j] - mean) * rs : 0.0f;
+        xh[v][j] = (xh[v][j] - mean) * rs;   // (behind the row's end g is 0)
         gw[v][j] = fmaf(g[v][j], xh[v][j], gw[v][j]);
         gb[v][j] += g[v][j];
         g[v][j] *= w[j];
@@ -483,14 +484,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
         sgx = fmaf(g[v][j], xh[v][j], sgx);
       }
     }
-    sg = warp_sum(sg);
-    sgx = warp_sum(sgx);
-    float(*rd)[32] = red[it & 1];
+    // both sums in one tree: after the first exchange the lower lanes carry sg, the upper sgx
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (a.wpr > 1 && lane == 0) {
-      rd[0][warp] = sg;
-      rd[1][warp] = sgx;
-    }
+    const bool upper = lane >= 16;
+    float both = (upper ? sgx : sg) + __shfl_xor_sync(0xffffffffu, upper ? sg : sgx, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
+    float(*rd)[32] = red[it & 1];
+    if (a.wpr > 1 && (lane & 15) == 0) rd[lane >> 4][warp] = both;
     __syncthreads();
     if (threadIdx.x == 0 && ok && it + S < rounds) fill(it + S, s);
     if (++s == S) {
@@ -498,10 +499,15 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) k_norm_bwd_ring(con
       parity ^= 1u;
     }
     if (a.wpr > 1) {
-      const int w0 = warp / a.wpr * a.wpr;
-      sg = warp_sum(lane < a.wpr ? rd[0][w0 + lane] : 0.0f);
-      sgx = warp_sum(lane < a.wpr ? rd[1][w0 + lane] : 0.0f);
+      const int w0 = warp / a.wpr * a.wpr, q = lane & 15;
+      both = q < a.wpr ? rd[lane >> 4][w0 + q] : 0.0f;
+      if (a.wpr > 16 && q + 16 < a.wpr) both += rd[lane >> 4][w0 + q + 16];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
     }
+    const float other = __shfl_xor_sync(0xffffffffu, both, 16);
+    sg = upper ? other : both;
+    sgx = upper ? both : other;
     const float c0 = a.layer ? sg * inv_n : 0.0f, c1 = sgx * inv_n;
     if (live) {
       R* gx = static_cast<R*>(a.g_x) + row * nvec;
