@@ -22,7 +22,7 @@ struct Epilogue {
 // The few-row products of k_linear_few.cu: C[T, N] = x [T, K] . w^T with the epilogue, w
 // stored [N, K], or [K, N] with w_mn.  apart: the kernel before it on the stream writes nothing
 // that this one touches, and its end may be waited for at this one's end.
-bool linear_few(int64_t M);
+bool linear_few(int64_t rows, int64_t contracted);
 cudaError_t run_linear_few(int64_t T, int64_t N, int64_t K, const void* x, const void* w, bool w_mn,
                            const Epilogue& ep, ErrFlags* err, bool clear_err, bool apart, Problem& p);
 

@@ -24,7 +24,7 @@
 // (`cpairs`): their float32 tiles meet in shared memory, each pair reads its share of the
 // columns from the others in rank order and finishes it.  Where more cuts pay
 // (`splits`), partial tiles go through global memory and k_linear_reduce adds them.
-// Products of up to 128 rows are k_linear_few's.
+// Products of few rows are k_linear_few's.
 #include <cuda.h>
 
 #include <atomic>
@@ -792,7 +792,9 @@ int gpre_tx(int64_t N) {
 int gpre_rows(int64_t M, int64_t N) {
   const int tx = gpre_tx(N);
   const int64_t col_ctas = (N + tx * 8 - 1) / (tx * 8), least = 4 * (kGpThreads / tx);
-  int64_t r = (M * col_ctas + 148 * 8 - 1) / (148 * 8);
+  // one wave of 5 CTAs an SM
+  const int64_t row_ctas = col_ctas < 148 * 5 ? 148 * 5 / col_ctas : 1;
+  int64_t r = (M + row_ctas - 1) / row_ctas;
   r = r < least ? least : r;
   if (r < (M + 65534) / 65535) r = (M + 65534) / 65535;   // grid y limit
   return (int)r;
@@ -818,7 +820,7 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int act, char* base) {
   w.gp = reinterpret_cast<__nv_bfloat16*>(take(act == JM_ACT_NONE ? 0 : (size_t)M * N * 2));
   const int64_t rows = M ? (M + gpre_rows(M, N) - 1) / gpre_rows(M, N) : 0;
   w.bias_part = reinterpret_cast<float*>(take((size_t)rows * N * 4));
-  const size_t px = M && !linear_few(M) ? part_bytes(M, K, N) : 0, pw = M ? part_bytes(N, K, M) : 0;
+  const size_t px = M && !linear_few(M, N) ? part_bytes(M, K, N) : 0, pw = M ? part_bytes(N, K, M) : 0;
   w.part = reinterpret_cast<float*>(take(px > pw ? px : pw));
   w.bytes = off;
   return w;
@@ -827,7 +829,7 @@ BwdWs bwd_ws(int64_t M, int64_t K, int64_t N, int act, char* base) {
 }  // namespace
 
 size_t linear_fwd_ws_bytes(int64_t M, int64_t K, int64_t N) {
-  return sizeof(ErrFlags) + (M && !linear_few(M) ? part_bytes(M, N, K) : 0);
+  return sizeof(ErrFlags) + (M && !linear_few(M, K) ? part_bytes(M, N, K) : 0);
 }
 
 size_t linear_bwd_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
@@ -844,7 +846,7 @@ cudaError_t run_linear_fwd(const LinearArgs& a, Problem& p) {
   ep.pre = static_cast<__nv_bfloat16*>(a.pre);
   ep.act = a.act;
   launches_begin(p);
-  if (linear_few(a.M))
+  if (linear_few(a.M, a.K))
     return run_linear_few(a.M, a.N, a.K, a.x, a.w, false, ep, err, true, false, p);
   return product<false, false>(a.M, a.N, a.K, a.x, a.w, ep,
                                reinterpret_cast<float*>(a.ws + sizeof(ErrFlags)), err, true, false, p);
@@ -890,7 +892,7 @@ cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
   if (a.g_x) {  // [M, K] = g_p [M, N] . w [N, K]
     ep.out = static_cast<__nv_bfloat16*>(a.g_x);
     // (apart from the bias's sums where these came last)
-    e = linear_few(a.M)
+    e = linear_few(a.M, a.N)
             ? run_linear_few(a.M, a.K, a.N, gp, a.w, true, ep, err, clear, a.g_bias != nullptr, p)
             : product<false, true>(a.M, a.K, a.N, gp, a.w, ep, w.part, err, clear,
                                    a.g_bias != nullptr, p);

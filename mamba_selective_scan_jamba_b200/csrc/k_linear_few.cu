@@ -2,7 +2,7 @@
 //   out[t, n] = act(sum_k x[t, k] w[n, k] + bias[n]) + residual[t, n]
 //   g_x[t, k] = sum_n g_p[t, n] w[n, k]
 //
-// With up to 256 rows the weights' bytes bound the product (one row of 4096 -> 16384:
+// With few rows the weights' bytes bound the product (one row of 4096 -> 16384:
 // 134 MB, 20 us of HBM time), so the weights are the MMA's A operand - 128 features are
 // the TMEM lanes - and the rows its N: no lane is wasted on rows that are not there, and
 // one row costs the tensor cores as little as 16.  In the gradient the contracted index
@@ -30,7 +30,6 @@ constexpr int kWBytes = kTile * kK * 2;
 constexpr int kMaxStages = 12;
 constexpr int kMaxCluster = 8;
 constexpr size_t kSmemSm = 227 * 1024;
-constexpr int64_t kFewRows = 128;      // above, k_linear_pair's 256-row tiles are not idle
 
 struct FewArgs {
   int T, nb;             // rows; rounded up to the MMA's N
@@ -164,9 +163,9 @@ __global__ void __launch_bounds__(kThreads)
         uint32_t r[16];
         tmem_ld16(tb + (uint32_t)c, r);
         tmem_ld_wait();
+        // (the tile's place holds whole blocks of 16 rows)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < g.T) tile[(c + i) * kTile + et] = __uint_as_float(r[i]);
+        for (int i = 0; i < 16; ++i) tile[(c + i) * kTile + et] = __uint_as_float(r[i]);
       }
     }
     tc_fence_before();
@@ -238,7 +237,7 @@ FewShape few_shape(int64_t T, int64_t N, int64_t K) {
   FewShape f{};
   f.nb = (int)(ceil_div(T, 16) * 16);
   const int64_t tiles = ceil_div(N, kTile), chunks = ceil_div(K, kK);
-  const size_t stage = kWBytes + (size_t)f.nb * 128, tile = (size_t)T * kTile * 4;
+  const size_t stage = kWBytes + (size_t)f.nb * 128, tile = (size_t)f.nb * kTile * 4;
   const double hbm = (double)N * (double)K * 2.0 / 6.5e6;
   double best = 1e30;
   for (int c = 1; c <= kMaxCluster; c *= 2) {
@@ -300,7 +299,13 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& x, const FewArgs
 
 }  // namespace
 
-bool linear_few(int64_t M) { return M <= kFewRows; }
+// Up to 64 rows, or 128 over a contracted index above 1024: a tile's exchange grows with the
+// rows, k_linear_pair's does not, but its 256-row tiles read the weights no faster for few
+// rows.  128 rows: 8192 -> 4096 18.8 us here, 20.8 us there; 1024 -> 1024 8.0 us here, 6.6 us
+// there; 160 rows: 8192 -> 4096 20.9 us both, 1024 -> 1024 9.5 us here, 6.6 us there.
+bool linear_few(int64_t rows, int64_t contracted) {
+  return rows <= 64 || (rows <= 128 && contracted > 1024);
+}
 
 cudaError_t run_linear_few(int64_t T, int64_t N, int64_t K, const void* x, const void* w, bool w_mn,
                            const Epilogue& ep, ErrFlags* err, bool clear_err, bool apart, Problem& p) {
