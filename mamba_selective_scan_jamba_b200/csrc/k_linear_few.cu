@@ -42,21 +42,6 @@ struct FewArgs {
   bool late_wait;   // wait for the kernel before this one at the end
 };
 
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
-__device__ __forceinline__ uint32_t rank_addr(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t n;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
@@ -188,7 +173,7 @@ __global__ void __launch_bounds__(kThreads)
     }
 #pragma unroll 4
     for (uint32_t q = 0; C > 1 && q < C; ++q) {
-      const uint32_t p = rank_addr(at, q);
+      const uint32_t p = cluster_addr(at, q);
       const float4 a = ld_cluster4(p), b = ld_cluster4(p + 16);
       v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;

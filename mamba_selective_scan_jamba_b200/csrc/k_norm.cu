@@ -631,13 +631,12 @@ template <typename Args>
 using NormKern = void (*)(const Args);
 
 // The kernel built for a shape's threads (rounded up to 256, 512 or 1024, which sets the
-// registers a thread may use).  16,384 columns need 4 vectors of 16 bytes a thread only in
-// float32, at 1024 threads; 4 and 8 values in narrower ones are for 128 and 2048 columns.
+// registers a thread may use): 2 vectors of 16 bytes a thread (4 only in float32 above 8192
+// columns, at 1024 threads), or 4, 8 (2048 columns at most) or 16 values in narrower ones.
 #define JMIX_NORM_FULL(KERN, T, FULL)                             \
-  (s.nv == 4             ? KERN<T, FULL, 16 / FULL, 1024>         \
-   : s.threads() <= 256  ? KERN<T, FULL, 2, 256>                  \
-   : s.threads() <= 512  ? KERN<T, FULL, 2, 512>                  \
-                         : KERN<T, FULL, 2, 1024>)
+  (s.threads() <= 256  ? KERN<T, FULL, 2, 256>                    \
+   : s.threads() <= 512 ? KERN<T, FULL, 2, 512>                   \
+                        : KERN<T, FULL, 2, 1024>)
 #define JMIX_NORM_NARROW(KERN, T, VEC)                            \
   (s.nv * VEC == 4       ? KERN<T, VEC, 4 / VEC, 256>             \
    : s.nv * VEC == 8     ? KERN<T, VEC, 8 / VEC, 256>             \
@@ -652,7 +651,7 @@ NormKern<NormFwdArgs> fwd_kernel(const NormShape& s, jm_dtype io) {
            : s.vec == 2 ? JMIX_NORM_NARROW(k_norm_fwd, __nv_bfloat16, 2)
                         : JMIX_NORM_NARROW(k_norm_fwd, __nv_bfloat16, 1);
   }
-  if (s.full) return JMIX_NORM_FULL(k_norm_fwd, float, 4);
+  if (s.full) return s.nv == 4 ? k_norm_fwd<float, 4, 4, 1024> : JMIX_NORM_FULL(k_norm_fwd, float, 4);
   return s.vec == 2 ? JMIX_NORM_NARROW(k_norm_fwd, float, 2)
                     : JMIX_NORM_NARROW(k_norm_fwd, float, 1);
 }
@@ -669,11 +668,10 @@ NormKern<NormBwdArgs> ring_kernel(const NormShape& s, jm_dtype io) {
                     : JMIX_NORM_NARROW(k_norm_bwd_ring, float, 1);
 }
 
+// (every aligned row but a float32 one above 8192 columns has a ring)
 NormKern<NormBwdArgs> bwd_kernel(const NormShape& s, jm_dtype io) {
-  if (io == JM_BF16)
-    return s.full ? JMIX_NORM_FULL(k_norm_bwd, __nv_bfloat16, 8)
-                  : JMIX_NORM_NARROW(k_norm_bwd, __nv_bfloat16, 1);
-  return s.full ? JMIX_NORM_FULL(k_norm_bwd, float, 4) : JMIX_NORM_NARROW(k_norm_bwd, float, 1);
+  if (io == JM_BF16) return JMIX_NORM_NARROW(k_norm_bwd, __nv_bfloat16, 1);
+  return s.full ? k_norm_bwd<float, 4, 4, 1024> : JMIX_NORM_NARROW(k_norm_bwd, float, 1);
 }
 #undef JMIX_NORM_FULL
 #undef JMIX_NORM_NARROW
