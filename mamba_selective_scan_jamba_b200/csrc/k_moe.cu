@@ -4,7 +4,7 @@
 //   h   = silu(x Wgate_e^T) (x Wup_e^T)     for each (token, chosen expert) pair
 //   out = sum_i g_i h_i Wdown_{e_i}^T + residual
 //
-// k_moe_route: one CTA per token; logits, choice, weights.
+// k_moe_route: one CTA, or with few tokens a cluster, per token; logits, choice, weights.
 // k_moe: one CTA per SM streams the chosen experts' weights once.  With few tokens
 // those bytes bound the layer (an expert of 4096 x 14336 is 352 MB: 54 us of HBM time,
 // its products for 32 tokens 7 us of tensor time), so the design keeps HBM busy:

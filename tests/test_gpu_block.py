@@ -240,3 +240,66 @@ def test_training_block(rows, d, f):
         torch.cuda.synchronize()
     for a, e in zip(t.results(), want):
         assert torch.equal(a, e)
+
+
+def test_many_calls_share_one_workspace():
+    """Calls of every operator follow one another without a wait, with one workspace between
+    them all: the bits of the same calls with a synchronisation after each."""
+    import random
+
+    import torch
+    from mamba_selective_scan_jamba_b200 import devio, jmix
+    calls, outs, need = [], [], 256
+
+    def buf(*like):
+        new = [torch.zeros_like(v) for v in like]
+        outs.extend(new)
+        return new
+
+    for m, k, n, a in ((1003, 264, 520, "relu"), (40, 512, 1024, "silu"), (4100, 72, 88, "gelu"),
+                       (300, 1024, 264, "none"), (1, 2048, 512, "silu"), (120, 1544, 392, "gelu")):
+        t = lin.make(m, k, n, seed=m)
+        d = jmix.linear_dims(m, k, n, act=lin.ACTS.index(a))
+        nf, nb = jmix.jm_linear_fwd_workspace_size(d), jmix.jm_linear_bwd_workspace_size(d)
+        need = max(need, nf, nb)
+        out, pre, gx, gw, gb = buf(t["r"], t["r"], t["x"], t["w"], t["b"])
+        calls.append(lambda w, t=t, d=d, n=nf, out=out, pre=pre: jmix.jm_linear_fwd(
+            d, t["x"], t["w"], out, w, n, bias=t["b"], residual=t["r"], pre=pre))
+        calls.append(lambda w, t=t, d=d, n=nb, a=a, pre=pre, gx=gx, gw=gw, gb=gb: jmix.jm_linear_bwd(
+            d, t["g"], t["x"], t["w"], w, n, pre=None if a == "none" else pre, g_x=gx, g_w=gw,
+            g_bias=gb))
+    for t_, d_, f_, e_ in ((1, 264, 1032, 4), (37, 512, 392, 8), (200, 64, 520, 2)):
+        m = moe.make(t_, d_, f_, e_, seed=t_)
+        d = jmix.moe_dims(t_, d_, f_, e_, 2, router=jmix.JM_ROUTE_SOFTMAX_TOPK)
+        n = jmix.jm_moe_fwd_workspace_size(d)
+        need = max(need, n)
+        out, = buf(m["x"])
+        calls.append(lambda w, m=m, d=d, n=n, out=out: jmix.jm_moe_fwd(
+            d, m["x"], m["wr"], m["wg"], m["wu"], m["wd"], out, w, n, residual=m["r"]))
+    for rows, cols, io in ((700, 1021, "f32"), (2000, 512, "bf16"), (64, 4096, "bf16")):
+        t = norm.make(rows, cols, io, seed=cols)
+        d = jmix.norm_dims(rows, cols, jmix.JM_BF16 if io == "bf16" else jmix.JM_F32, 1)
+        n = jmix.jm_norm_bwd_workspace_size(d)
+        need = max(need, n)
+        y, gx, gw, gb = buf(t["x"], t["x"], t["w"], t["w"])
+        st = torch.zeros(rows, 2, device="cuda")
+        calls.append(lambda w, t=t, d=d, n=n, y=y, st=st, gx=gx, gw=gw, gb=gb: (
+            jmix.jm_norm_fwd(d, t["x"], t["w"], y, bias=t["b"], stats=st),
+            jmix.jm_norm_bwd(d, t["gy"], t["x"], t["w"], st, gx, w, n, g_sum=t["gs"], g_weight=gw,
+                             g_bias=gb)))
+    ws = devio.workspace(need)
+    for c in calls:
+        c(ws)
+        torch.cuda.synchronize()
+        assert jmix.jm_poll_error(ws) == jmix.JM_OK
+    want = [v.clone() for v in outs]
+    rng = random.Random(2)
+    for _ in range(6):
+        # (pre holds the same values from the first pass on, so any order will do)
+        order = list(range(len(calls)))
+        rng.shuffle(order)
+        for i in order:
+            calls[i](ws)
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
