@@ -604,9 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  // (partial tiles cost the first phase a round of counting and of h, 4 us; the second
-  // sums them where it has to wait anyway)
-  const Line line[2] = {make_line(L.n_entries, a.F, a.D, 128, 4.0f, 8),
+  // Partial tiles cost the first phase a round of counting and of h, 4 us, and their sums
+  // more with more rows (53 tokens, 2 experts of 2208 x 1864: 8 parts at most 36 us, 4 33
+  // us); the second sums them where it has to wait anyway.
+  const Line line[2] = {make_line(L.n_entries, a.F, a.D, 128, 4.0f, a.NB <= 32 ? 8 : 4),
                         make_line(L.n_entries, a.D, a.F, 256, 1.0f, 16)};
 
   if (warp == 0) {
