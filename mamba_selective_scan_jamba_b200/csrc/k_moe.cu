@@ -19,10 +19,10 @@
 // * A unit inside one CTA's range is finished from TMEM.  A cut one leaves float32
 //   partial tiles, each CTA of it then finishing its share of the columns; partial tiles
 //   are added in CTA order, so results do not depend on timing.
-// * Warp 0 streams weights, warp 6 the tokens' rows (gathered by index, then rows of h),
-//   warp 1 issues the MMAs, warps 2-5 drain them.  Nothing but warp 6 waits between the
-//   phases, and only for h of the block it needs, so the ring is full of
-//   down-projection weights when h arrives.
+// * Warp 0 streams weights, warps 6 and 7 half of the tokens' rows each (gathered by index 4
+//   at a time, some 45 cycles of one thread, then rows of h), warp 1 issues the MMAs, warps
+//   2-5 drain them.  Nothing but warps 6 and 7 waits between the phases, and only for h of
+//   the block they need, so the ring is full of down-projection weights when h arrives.
 //
 // CTAs wait for one another (partial tiles, h, the last sum), so the launch is
 // cooperative; every wait is bounded and reports to the error header.
@@ -37,7 +37,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRouteThreads = 512;
 constexpr int kK = 64;                          // K per step: one 128-byte swizzle span
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int out_flag;
-  __shared__ int4 gather_rows[32];   // token rows of the block, 4 a gather
+  __shared__ int4 gather_rows[2][32];   // token rows of the block, 4 a gather
   Lists& L = *reinterpret_cast<Lists*>(smem + S * stage_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t tmem_cols = 64;   // two accumulators of two row groups
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&full[s]), 2);    // weights' and tokens' producers
+      mbar_init(smem_u32(&full[s]), 3);    // the weights' and two of the tokens' producers
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -667,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 6) {
+  } else if (warp >= 6) {
+    const int half = warp - 6;
     const uint32_t base = smem_u32(smem) + kWBytes;
     Place at;
     bool ok = true;
@@ -675,7 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned have = ~0u;   // the block whose h is known to be there, or whose rows are held
       for (Walk w(line[ph]); ok && w.more(); w.next()) {
         const Entry en = L.entry[w.ent];
-        const int n16 = (en.n + 15) / 16;
+        // this warp's blocks of 16 rows
+        const int n16 = (en.n + 15) / 16, b0 = half ? (n16 + 1) / 2 : 0;
+        const int b1 = half ? n16 : (n16 + 1) / 2;
         if (w.ent != have) {
           have = w.ent;
           if (ph == 0) {
@@ -683,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             const uint16_t* tok = L.token + en.r0;
             const int r = lane * 4, last = en.n - 1;
-            gather_rows[lane] = make_int4(tok[min(r, last)], tok[min(r + 1, last)],
-                                          tok[min(r + 2, last)], tok[min(r + 3, last)]);
+            gather_rows[half][lane] = make_int4(tok[min(r, last)], tok[min(r + 1, last)],
+                                                tok[min(r + 2, last)], tok[min(r + 3, last)]);
             __syncwarp();
           } else {
             ok = warp_wait(&a.sync->ready[w.ent], line[0].tiles * line[0].ksteps, a.err, 93);
@@ -702,16 +705,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             const uint32_t fb = smem_u32(&full[p.s]), dst = base + p.s * stage_bytes;
-            mbar_arrive_expect_tx(fb, (uint32_t)(n16 * 16 * 128));
+            mbar_arrive_expect_tx(fb, (uint32_t)((b1 - b0) * 16 * 128));
             if (ph == 0) {
-#pragma unroll 2
-              for (int q = 0; q < n16 * 4; q += 2) {   // 4 rows by index at a time
-                const int4 t = gather_rows[q], u = gather_rows[q + 1];
+              for (int q = b0 * 4; q < b1 * 4; q += 2) {   // 4 rows by index at a time
+                const int4 t = gather_rows[half][q], u = gather_rows[half][q + 1];
                 tma_gather4(dst + q * 512, &tm_x, fb, k, t.x, t.y, t.z, t.w);
                 tma_gather4(dst + q * 512 + 512, &tm_x, fb, k, u.x, u.y, u.z, u.w);
               }
             } else {
-              for (int q = 0; q < n16; ++q) tma_load_2d(dst + q * 2048, &tm_h, fb, k, en.r0 + q * 16);
+              for (int q = b0; q < b1; ++q) tma_load_2d(dst + q * 2048, &tm_h, fb, k, en.r0 + q * 16);
             }
           }
         }
@@ -940,7 +942,7 @@ int moe_block(int64_t T, int64_t E, int64_t k) {
 }
 
 constexpr size_t kSmemMost = 227 * 1024;
-constexpr size_t kStaticMost = 1024;  // barriers, flags and gather rows
+constexpr size_t kStaticMost = 1536;  // barriers, flags and gather rows
 constexpr size_t kListBytes = (sizeof(Lists) + 255) / 256 * 256;
 
 int ring_stages(int nb) {
