@@ -55,17 +55,36 @@ struct Entry {
   uint16_t e, r0, n, pad;
 };
 
-// Routing lists, rebuilt by every CTA in shared memory.  Pair rows (token, choice) are
-// sorted by expert, tokens ascending.
+// Routing lists, rebuilt by every CTA in shared memory, of the call's sizes (what they do not
+// take is the ring's).  Pair rows (token, choice) are sorted by expert, tokens ascending.
 struct Lists {
-  Entry entry[kMaxEntries];
-  uint16_t token[kMaxPairs];     // of a pair row
-  uint16_t ent[kMaxPairs];       // block of a pair row
-  uint16_t row[kMaxPairs];       // pair row of token * top_k + choice
-  int count[kMaxExperts];
-  int first[kMaxExperts];        // first pair row of an expert
-  uint16_t block[kMaxExperts];   // first block of an expert
-  int n_entries;
+  Entry* entry;
+  int* count;        // [E]
+  int* first;        // [E] first pair row of an expert
+  int* n_entries;
+  uint16_t* token;   // [P] of a pair row
+  uint16_t* ent;     // [P] block of a pair row
+  uint16_t* row;     // [P] pair row of token * top_k + choice
+  uint16_t* block;   // [E] first block of an expert
+  __device__ __forceinline__ Lists(uint8_t* at, int P, int E, int NB) {
+    entry = reinterpret_cast<Entry*>(at);
+    count = reinterpret_cast<int*>(entry + most_entries(P, E, NB));
+    first = count + E;
+    n_entries = first + E;
+    token = reinterpret_cast<uint16_t*>(n_entries + 1);
+    ent = token + P;
+    row = ent + P;
+    block = row + P;
+  }
+  // every expert's last block, and the full ones before them
+  static __host__ __device__ int most_entries(int P, int E, int NB) {
+    return (E < P ? E : P) + P / NB;
+  }
+  static size_t bytes(int P, int E, int NB) {
+    const size_t n = sizeof(Entry) * most_entries(P, E, NB) + 4 * (2 * (size_t)E + 1) +
+                     2 * (3 * (size_t)P + E);
+    return (n + 255) / 256 * 256;
+  }
 };
 
 // Counters that k_moe_route clears.
@@ -354,7 +373,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const MoeKArgs a) {
 // The lists of every CTA from the choices: a counting sort by expert.  `scratch` (the
 // ring, not in use yet): [chunks of 32 pairs][E] counts, then each pair's expert and its
 // place among its chunk's.
-__device__ void build_lists(const MoeKArgs& a, Lists& L, uint16_t* scratch) {
+__device__ void build_lists(const MoeKArgs& a, const Lists& L, uint16_t* scratch) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = a.T * a.topk, chunks = (P + 31) / 32;
   uint16_t* hist = scratch;
@@ -409,7 +428,7 @@ __device__ void build_lists(const MoeKArgs& a, Lists& L, uint16_t* scratch) {
       rows += __shfl_sync(0xffffffffu, r, 31);
       blocks += __shfl_sync(0xffffffffu, b, 31);
     }
-    if (lane == 0) L.n_entries = blocks;
+    if (lane == 0) *L.n_entries = blocks;
   }
   __syncthreads();
   for (int p = tid; p < P; p += kThreads) {
@@ -601,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int out_flag;
   __shared__ int4 gather_rows[2][32];   // token rows of the block, 4 a gather
-  Lists& L = *reinterpret_cast<Lists*>(smem + S * stage_bytes);
+  const Lists L(smem + S * stage_bytes, a.T * a.topk, a.E, a.NB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t tmem_cols = 64;   // two accumulators of two row groups
   while (tmem_cols < 4u * a.NB) tmem_cols *= 2;
@@ -635,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Partial tiles cost the first phase a round of counting and of h, 4 us, and their sums
   // more with more rows (53 tokens, 2 experts of 2208 x 1864: 8 parts at most 36 us, 4 33
   // us); the second sums them where it has to wait anyway.
-  const Line line[2] = {make_line(L.n_entries, a.F, a.D, 128, 4.0f, a.NB <= 32 ? 8 : 4),
-                        make_line(L.n_entries, a.D, a.F, 256, 1.0f, 16)};
+  const Line line[2] = {make_line(*L.n_entries, a.F, a.D, 128, 4.0f, a.NB <= 32 ? 8 : 4),
+                        make_line(*L.n_entries, a.D, a.F, 256, 1.0f, 16)};
 
   if (warp == 0) {
     if (elect_one()) {
@@ -943,15 +962,13 @@ int moe_block(int64_t T, int64_t E, int64_t k) {
 
 constexpr size_t kSmemMost = 227 * 1024;
 constexpr size_t kStaticMost = 1536;  // barriers, flags and gather rows
-constexpr size_t kListBytes = (sizeof(Lists) + 255) / 256 * 256;
-
-int ring_stages(int nb) {
-  const size_t n = (kSmemMost - kStaticMost - 1024 - kListBytes) / (kWBytes + nb * 128);
+int ring_stages(int nb, size_t lists) {
+  const size_t n = (kSmemMost - kStaticMost - 1024 - lists) / (kWBytes + nb * 128);
   return n > kMaxStages ? kMaxStages : (int)n;
 }
 
-size_t ring_smem(int nb) {
-  return 1024 + ring_stages(nb) * (size_t)(kWBytes + nb * 128) + kListBytes;
+size_t ring_smem(int nb, size_t lists) {
+  return 1024 + ring_stages(nb, lists) * (size_t)(kWBytes + nb * 128) + lists;
 }
 
 struct MoeWs {
@@ -1024,7 +1041,8 @@ cudaError_t run_moe(const MoeArgs& m, Problem& p) {
   a.D = (int)m.D;
   a.F = (int)m.F;
   a.NB = moe_block(m.T, m.E, m.topk);
-  a.stages = ring_stages(a.NB);
+  const size_t lists = Lists::bytes(a.T * a.topk, a.E, a.NB);
+  a.stages = ring_stages(a.NB, lists);
   a.topk_softmax = m.topk_softmax;
   a.x = static_cast<const __nv_bfloat16*>(m.x);
   a.wr = static_cast<const __nv_bfloat16*>(m.router_w);
@@ -1067,7 +1085,7 @@ cudaError_t run_moe(const MoeArgs& m, Problem& p) {
   attr[1].val.cooperative = 1;
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = ring_smem(a.NB);
+  cfg.dynamicSmemBytes = ring_smem(a.NB, lists);
   e = cudaLaunchKernelEx(&cfg, k_moe, wg, wu, wd, tx, th, a);
   if (e == cudaSuccess) launched(p, "k_moe");
   return e;
