@@ -20,9 +20,9 @@
 // swizzled shared memory, two buffers a group; the residual comes into the same place by
 // TMA before the accumulator is complete, and TMA stores write whole lines.
 //
-// Problems with few tiles are cut along K.  Up to 4 pairs of a cluster share a tile
-// (`cpairs`): their float32 tiles meet in shared memory, each pair reads its share of the
-// columns from the others in rank order and finishes it.  Where more cuts pay
+// Problems with few tiles are cut along K.  Two pairs of a cluster may share a tile
+// (`cpairs`): their float32 tiles meet in shared memory, each pair reads its half of the
+// columns from both in rank order and finishes it.  Where more cuts pay
 // (`splits`), partial tiles go through global memory and k_linear_reduce adds them.
 // Products of few rows are k_linear_few's.
 #include <cuda.h>
@@ -566,23 +566,23 @@ __global__ void __launch_bounds__(kGpThreads)
   }
 }
 
-// Column sums of the partial rows in a fixed order (16 interleaved chains).
-__global__ void __launch_bounds__(512)
+// Column sums of the partial rows in a fixed order (32 interleaved chains).
+__global__ void __launch_bounds__(1024)
     k_linear_bias_reduce(const float* __restrict__ part, int64_t rows, int64_t N,
                          __nv_bfloat16* __restrict__ g_bias) {
-  __shared__ float sh[16][33];
+  __shared__ float sh[32][33];
   grid_dep_wait();
   grid_dep_launch();
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float acc = 0.0f;
   if (c < N)
 #pragma unroll 4
-    for (int64_t r = threadIdx.y; r < rows; r += 16) acc += part[r * N + c];
+    for (int64_t r = threadIdx.y; r < rows; r += 32) acc += part[r * N + c];
   sh[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
   if (threadIdx.y == 0 && c < N) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) acc += sh[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) acc += sh[i][threadIdx.x];
     g_bias[c] = __float2bfloat16_rn(acc);
   }
 }
@@ -623,31 +623,30 @@ struct Cut {
 };
 
 // Estimated microseconds: waves of work items on 74 pairs (a 64-wide chunk of a 256 x
-// 256 tile takes a pair 0.27 us, of a 256 x 128 tile 0.16), ~2 us for the first fill and
-// last drain; 2 us for a cluster's exchange; for splits the partial tiles' round trip
-// through L2 and one launch.
+// 256 tile takes a pair 0.28 us, of a 256 x 128 tile 0.16); 2.5 or 3.5 us for a cluster's
+// exchange; for splits the partial tiles' round trip through L2 and one launch.  (Clusters of
+// 4 pairs took 7.5 us more than no exchange, more than splits: 600 x 2048 x 512 in 14.1 us,
+// with 4 splits in 8.6.  256 x 8192 x 4096: two pairs 21.3 us, two splits 23.2.)
 Cut choose_cut(int64_t M, int64_t N, int64_t K) {
   const int64_t chunks = (K + kK - 1) / kK;
   Cut best{256, 1, 1};
   double best_us = 1e30;
   for (int bn = 256; bn >= 128; bn /= 2) {
     const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn);
-    const double chunk_us = bn == 256 ? 0.27 : 0.16;
     for (int s = 1; s <= 16; ++s) {
       if (s > 1 && chunks / s < 2) break;
       const int64_t waves = (tiles * s + kPairs - 1) / kPairs;
-      const double us = (double)waves * (double)((chunks + s - 1) / s) * chunk_us + 2.0;
-      // (a cluster's pairs take equal shares of at least 64 columns; a B200 holds 33 clusters
-      // of 4 CTAs or 15 of 8 with one CTA an SM)
-      if (s == 1 || (s == 2 && tiles <= 33) || (s == 4 && bn == 256 && tiles <= 15)) {
-        const double c = us + (s > 1 ? 2.0 : 0.0);
+      const double us = (double)(waves * ((chunks + s - 1) / s)) * (bn == 256 ? 0.28 : 0.16);
+      // (a B200 holds 33 clusters of 4 CTAs with one CTA an SM)
+      if (s == 1 || (s == 2 && tiles <= 33)) {
+        const double c = us + (s == 1 ? 0.0 : bn == 256 ? 3.5 : 2.5);
         if (c < best_us * 0.999) {
           best_us = c;
           best = {bn, s, 1};
         }
       }
       if (s > 1) {
-        const double m = us + 5.0 + (double)M * (double)N * 4.0 * (2 * s + 1) / 6.0e6;
+        const double m = us + 1.5 + (double)M * (double)N * 4.0 * (2 * s + 1) / 6.0e6;
         if (m < best_us * 0.999) {
           best_us = m;
           best = {bn, 1, s};
@@ -769,9 +768,20 @@ cudaError_t product(int64_t M, int64_t N, int64_t K, const void* A, const void* 
 // Threads of a CTA of k_linear_gpre along the columns (a power of two), and rows a CTA
 // takes: enough CTAs for the GPU, at least 4 rows a thread.
 int gpre_tx(int64_t N) {
-  int tx = 8;
-  while (tx < kGpThreads && tx * 8 < N) tx *= 2;
-  return tx;
+  // the widest that leaves fewest columns behind the matrix's end, down to 512 bytes a row
+  // (the whole backward at 4847 x 64 -> 2440, whose second column of CTAs was 81% idle at 256,
+  // and with cuts of its products: 60 -> 45 us)
+  int best = 32;
+  double most = 0.0;
+  for (int tx = kGpThreads; tx >= 32; tx /= 2) {
+    const double used = (double)N / (double)((N + tx * 8 - 1) / (tx * 8) * (tx * 8));
+    if (used > most * 1.05) {
+      most = used;
+      best = tx;
+    }
+  }
+  while (best > 8 && best * 4 >= N) best /= 2;   // a narrow matrix
+  return best;
 }
 
 int gpre_rows(int64_t M, int64_t N) {
@@ -862,7 +872,7 @@ cudaError_t run_linear_bwd(const LinearArgs& a, Problem& p) {
     launched(p, "k_linear_gpre");
     if (grad) gp = w.gp;
     if (a.g_bias) {
-      e = launch(k_linear_bias_reduce, dim3((unsigned)((a.N + 31) / 32)), dim3(32, 16), 0, 1, p.stream,
+      e = launch(k_linear_bias_reduce, dim3((unsigned)((a.N + 31) / 32)), dim3(32, 32), 0, 1, p.stream,
                  (const float*)w.bias_part, (int64_t)grid.y, a.N,
                  static_cast<__nv_bfloat16*>(a.g_bias));
       if (e != cudaSuccess) return e;
