@@ -81,7 +81,22 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot, base = smem_u32(smem);
-  if (!g.late_wait) grid_dep_wait();
+  if (!g.late_wait) {
+    // The ring's first weights on their way to L2 while the kernel before ends (L2 sees what
+    // that one still writes; shared memory would not).  1 x 4096 -> 16384: 24.4 -> 22.4 us,
+    // 16 x 14336 -> 4096 22.3 -> 20.6; twice the ring's is slower between other kernels (norm,
+    // 1 x 4096 -> 16384, back: 48.5 -> 51.5 us), and k_linear_pair gains nothing by it.
+    if (warp == 0 && elect_one())
+      for (int kc = k0; kc < k1 && kc < k0 + S; ++kc) {
+        if constexpr (AMN) {
+          tma_prefetch_3d(&tm_w, (int32_t)n0, kc * kK, 0);
+          tma_prefetch_3d(&tm_w, (int32_t)n0 + 64, kc * kK, 0);
+        } else {
+          tma_prefetch_3d(&tm_w, kc * kK, (int32_t)n0, 0);
+        }
+      }
+    grid_dep_wait();
+  }
   grid_dep_launch();
   // (a wait gives up after 2 s: no CTA can have recorded one yet)
   if (g.clear_err && blockIdx.x == 0 && tid < (int)(sizeof(ErrFlags) / 4))
