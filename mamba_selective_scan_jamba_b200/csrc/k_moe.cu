@@ -114,11 +114,15 @@ struct MoeKArgs {
 // A phase's line of work: units of `ksteps` steps in `ppu` parts of `quant` steps (the last
 // one may have fewer), the parts cut between `ctas` CTAs.
 struct Line {
-  unsigned tiles, ksteps, total, quant, ppu, parts, ctas;
-  double inv;   // 1 / parts
-  __device__ __forceinline__ unsigned start(unsigned c) const {
-    const unsigned p = (unsigned)((uint64_t)parts * min(c, ctas) / ctas), u = p / ppu;
-    return u * ksteps + (p - u * ppu) * quant;
+  unsigned tiles, ksteps, quant, ppu, parts, ctas;
+  unsigned base, rest;   // parts = base ctas + rest
+  float inv_ctas;
+  double inv;            // 1 / parts
+  // the first part of CTA c's range: floor(c parts / ctas).  (c rest is below 2^16 and the
+  // quotient's distance from an integer at least 0.5 / 160: float32 is exact.)
+  __device__ __forceinline__ unsigned first_part(unsigned c) const {
+    c = min(c, ctas);
+    return c * base + (unsigned)(((float)(c * rest) + 0.5f) * inv_ctas);
   }
   // the CTA whose range holds the part p: ((p + 1) ctas - 1) / parts (below 2^32, checked
   // on the host; by a multiplication, which may be one off)
@@ -146,26 +150,31 @@ struct Line {
 // somebody has to add them all (2 units of 64 steps cut into single ones: 35 us).  There are
 // no more CTAs than parts, so that no range between two others is empty.
 __device__ __forceinline__ Line make_line(unsigned entries, unsigned rows, unsigned kdim,
-                                          unsigned tile_rows, float join_us, unsigned most) {
+                                          unsigned tile_rows, float join_us, unsigned log2_most) {
   Line l;
   l.tiles = (rows + tile_rows - 1) / tile_rows;
   l.ksteps = (kdim + kK - 1) / kK;
   const unsigned units = entries * l.tiles;
-  l.total = units * l.ksteps;
+  const unsigned total = units * l.ksteps;
   const unsigned rounds = units / gridDim.x, rest = units - rounds * gridDim.x;
   const float all = (float)(rounds * gridDim.x * l.ksteps) * 0.005f, k = (float)l.ksteps;
   const float whole = fmaxf(all, (float)(rounds * l.ksteps) * 0.55f) +
                       (rest ? fmaxf((float)rest * k * 0.005f, k * 0.55f) : 0.0f);
-  const unsigned least = (l.ksteps + most - 1) / most;   // steps of a part
-  const float cut = fmaxf((float)l.total * 0.005f,
-                          fmaxf((float)l.total / (float)gridDim.x, (float)least) * 0.55f);
+  const unsigned least = (l.ksteps + (1u << log2_most) - 1) >> log2_most;   // steps of a part
+  const float cut = fmaxf((float)total * 0.005f,
+                          fmaxf((float)total / (float)gridDim.x, (float)least) * 0.55f);
   l.quant = whole <= cut + join_us          ? l.ksteps
-            : l.total >= least * gridDim.x  ? 1u     // ranges of `least` steps by themselves
+            : total >= least * gridDim.x  ? 1u     // ranges of `least` steps by themselves
                                             : least;
   l.ppu = (l.ksteps + l.quant - 1) / l.quant;
   l.parts = units * l.ppu;
   l.ctas = max(min(gridDim.x, l.parts), 1u);
-  l.inv = 1.0 / (double)max(l.parts, 1u);
+  l.base = l.parts / l.ctas;
+  l.rest = l.parts - l.base * l.ctas;
+  l.inv_ctas = 1.0f / (float)l.ctas;
+  // (one Newton step from float32: a division in float64 would hold up the first loads)
+  const double n = (double)max(l.parts, 1u), r = (double)(1.0f / (float)max(l.parts, 1u));
+  l.inv = r * (2.0 - n * r);
   return l;
 }
 
@@ -173,11 +182,13 @@ __device__ __forceinline__ Line make_line(unsigned entries, unsigned rows, unsig
 // one or two in each step of the producing thread a step took it 550 ns).
 struct Walk {
   unsigned s, s1, ent, tile, k, ksteps, tiles;
-  __device__ __forceinline__ Walk(const Line& l) : ksteps(l.ksteps), tiles(l.tiles) {
-    s = l.start(blockIdx.x);
-    s1 = l.start(blockIdx.x + 1);
-    const unsigned u = s / ksteps;
-    k = s - u * ksteps;
+  Walk() = default;
+  __device__ __forceinline__ explicit Walk(const Line& l) : ksteps(l.ksteps), tiles(l.tiles) {
+    const unsigned p = l.first_part(blockIdx.x), p1 = l.first_part(blockIdx.x + 1);
+    const unsigned u = p / l.ppu, u1 = p1 / l.ppu;
+    k = (p - u * l.ppu) * l.quant;
+    s = u * ksteps + k;
+    s1 = u1 * ksteps + (p1 - u1 * l.ppu) * l.quant;
     ent = u / tiles;
     tile = u - ent * tiles;
   }
@@ -373,7 +384,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const MoeKArgs a) {
 // The lists of every CTA from the choices: a counting sort by expert.  `scratch` (the
 // ring, not in use yet): [chunks of 32 pairs][E] counts, then each pair's expert and its
 // place among its chunk's.
-__device__ void build_lists(const MoeKArgs& a, const Lists& L, uint16_t* scratch) {
+__device__ void build_lists(const MoeKArgs& a, const Lists& L, uint16_t* scratch, Line* line,
+                            Walk* walk) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = a.T * a.topk, chunks = (P + 31) / 32;
   uint16_t* hist = scratch;
@@ -431,6 +443,18 @@ __device__ void build_lists(const MoeKArgs& a, const Lists& L, uint16_t* scratch
     if (lane == 0) *L.n_entries = blocks;
   }
   __syncthreads();
+  if (warp >= 6) {   // the phases' lines and this CTA's ranges
+    // Partial tiles cost the first phase a round of counting and of h, 4 us, and their sums
+    // more with more rows (53 tokens, 2 experts of 2208 x 1864: 8 parts at most 36 us, 4 33
+    // us); the second sums them where it has to wait anyway.
+    const Line l = warp == 6 ? make_line(*L.n_entries, a.F, a.D, 128, 4.0f, a.NB <= 32 ? 3 : 2)
+                             : make_line(*L.n_entries, a.D, a.F, 256, 1.0f, 4);
+    const Walk w(l);
+    if (lane == 0) {
+      line[warp - 6] = l;
+      walk[warp - 6] = w;
+    }
+  }
   for (int p = tid; p < P; p += kThreads) {
     const int e = expert[p], at = hist[(p >> 5) * a.E + e] + place[p], r = L.first[e] + at;
     L.token[r] = (uint16_t)(p / a.topk);
@@ -438,7 +462,9 @@ __device__ void build_lists(const MoeKArgs& a, const Lists& L, uint16_t* scratch
     L.row[p] = (uint16_t)r;
   }
   fence_proxy_async_smem();   // TMA writes over the scratch
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
 }
 
 // Partial tile of CTA `cta` in phase `ph`: of the unit that starts before its range
@@ -620,6 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int out_flag;
   __shared__ int4 gather_rows[2][32];   // token rows of the block, 4 a gather
+  __shared__ Line line[2];   // of the phases
+  __shared__ Walk walk[2];
   const Lists L(smem + S * stage_bytes, a.T * a.topk, a.E, a.NB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t tmem_cols = 64;   // two accumulators of two row groups
@@ -646,16 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   grid_dep_wait();
-  build_lists(a, L, reinterpret_cast<uint16_t*>(smem));
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  build_lists(a, L, reinterpret_cast<uint16_t*>(smem), line, walk);
   const uint32_t tmem = tmem_slot;
-  // Partial tiles cost the first phase a round of counting and of h, 4 us, and their sums
-  // more with more rows (53 tokens, 2 experts of 2208 x 1864: 8 parts at most 36 us, 4 33
-  // us); the second sums them where it has to wait anyway.
-  const Line line[2] = {make_line(*L.n_entries, a.F, a.D, 128, 4.0f, a.NB <= 32 ? 8 : 4),
-                        make_line(*L.n_entries, a.D, a.F, 256, 1.0f, 16)};
 
   if (warp == 0) {
     if (elect_one()) {
@@ -664,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Place at;
       bool ok = true;
       for (int ph = 0; ok && ph < 2; ++ph) {
-        for (Walk w(line[ph]); ok && w.more(); w.next()) {
+        for (Walk w = walk[ph]; ok && w.more(); w.next()) {
           const int e = L.entry[w.ent].e, row = (int)w.tile * (ph == 0 ? 128 : 256);
           int k = (int)w.k * kK;
           for (unsigned n = w.steps(); n > 0; --n, k += kK, at.next(S)) {
@@ -693,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int ph = 0; ok && ph < 2; ++ph) {
       unsigned have = ~0u;   // the block whose h is known to be there, or whose rows are held
-      for (Walk w(line[ph]); ok && w.more(); w.next()) {
+      for (Walk w = walk[ph]; ok && w.more(); w.next()) {
         const Entry en = L.entry[w.ent];
         // this warp's blocks of 16 rows
         const int n16 = (en.n + 15) / 16, b0 = half ? (n16 + 1) / 2 : 0;
@@ -742,11 +762,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t base = smem_u32(smem);
+      const uint64_t ring = sw128_kmajor_desc(smem_u32(smem));
       Place at, acc;
       bool ok = true;
       for (int ph = 0; ok && ph < 2; ++ph) {
-        for (Walk w(line[ph]); ok && w.more(); w.next(), acc.next(2)) {
+        for (Walk w = walk[ph]; ok && w.more(); w.next(), acc.next(2)) {
           const int n16 = (L.entry[w.ent].n + 15) / 16;
           const uint32_t idesc = idesc_bf16_f32(128, n16 * 16);
           if (!mbar_wait(smem_u32(&acc_empty[acc.s]), acc.parity ^ 1u, a.err, 95)) {
@@ -762,14 +782,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
-            const uint32_t wa = base + at.s * stage_bytes, xb = wa + kWBytes;
+            const uint64_t wd = ring + at.s * (unsigned)(stage_bytes / 16);
 #pragma unroll
             for (int g = 0; g < 2; ++g)
 #pragma unroll
               for (int kk = 0; kk < kK / 16; ++kk)
-                umma_f16(d + (uint32_t)(g * a.NB),
-                         sw128_kmajor_desc(wa + g * kSlabBytes + kk * 32),
-                         sw128_kmajor_desc(xb + kk * 32), idesc, kk > 0 ? 1u : add);
+                umma_f16(d + (uint32_t)(g * a.NB), wd + (g * kSlabBytes + kk * 32) / 16,
+                         wd + (kWBytes + kk * 32) / 16, idesc, kk > 0 ? 1u : add);
             add = 1u;
             umma_commit(smem_u32(&empty[at.s]));
           }
@@ -783,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int ph = 0; ok && ph < 2; ++ph) {
       const Line& l = line[ph];
-      for (Walk w(l); w.more(); w.next(), acc.next(2)) {
+      for (Walk w = walk[ph]; w.more(); w.next(), acc.next(2)) {
         const unsigned ent = w.ent, tile = w.tile, b = acc.s;
         const bool whole = w.whole();
         const Entry en = L.entry[ent];
@@ -841,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The cut units this CTA took part in are its first and its last.
         unsigned cut_u[2], cut_steps[2], block = ~0u, done = 0;
         int cuts = 0;
-        for (Walk w(l); ok && w.more(); w.next()) {
+        for (Walk w = walk[ph]; ok && w.more(); w.next()) {
           const unsigned u = w.ent * w.tiles + w.tile;
           if (w.whole()) {   // counted for all units of a block at once
             if (w.ent != block && done) {
