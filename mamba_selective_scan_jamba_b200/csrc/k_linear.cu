@@ -21,8 +21,9 @@
 // TMA before the accumulator is complete, and TMA stores write whole lines.
 //
 // Problems with few tiles are cut along K.  Two pairs of a cluster may share a tile
-// (`cpairs`): their float32 tiles meet in shared memory, each pair reads its half of the
-// columns from both in rank order and finishes it.  Where more cuts pay
+// (`cpairs`): each writes the other's half of the columns, float32, into the other's shared
+// memory and finishes its own (256 x 8192 x 4096 with the residual: 20.1 us; with whole
+// tiles left for the other to read 21.3 us, 2 us of them these reads).  Where more cuts pay
 // (`splits`), partial tiles go through global memory and k_linear_reduce adds them.
 // Products of few rows are k_linear_few's.
 #include <cuda.h>
@@ -54,15 +55,17 @@ constexpr int stage_bytes(int BN) { return kABytes + b_bytes(BN); }
 constexpr int kRegion = 224 * 1024;
 constexpr int kMaxStages = kRegion / stage_bytes(128);
 constexpr int kStaging = 4 * kOutBytes;
-constexpr int stages(int BN, bool single) {
-  return (single ? kRegion : kRegion - kStaging) / stage_bytes(BN);
+// (the half tile that the other pair of a cluster sends lies behind the ring)
+constexpr int joined_bytes(int BN) { return BN / 2 * kHalf * 4; }
+constexpr int stages(int BN, bool single, bool joined) {
+  return (single ? kRegion - (joined ? joined_bytes(BN) : 0) : kRegion - kStaging) / stage_bytes(BN);
 }
 constexpr int kSmemBytes = 1024 + kRegion + 8 * (2 * kMaxStages + 6) + 16;
 
 struct PairArgs {
   int64_t M, N, K;
   unsigned m_tiles, n_tiles;
-  int cpairs;    // pairs of a cluster, each a range of the tile's K
+  int cpairs;    // pairs of a cluster (1 or 2), each a range of the tile's K
   int splits;    // above 1 (cpairs 1): float32 partial tiles [splits][M][N] through tm_out
   Epilogue ep;   // (its out and residual are reached through the maps)
   ErrFlags* err;
@@ -262,12 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tm_res,
                   const __grid_constant__ CUtensorMap tm_pre, const PairArgs g) {
   constexpr int kStage = stage_bytes(BN), kBHalf = BN / 2;
-  const int S = stages(BN, g.single);
+  const int S = stages(BN, g.single, g.cpairs > 1);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) __nv_bfloat16 bias_of[2][256];   // [group][tile parity][chunk][64]
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  // (behind the float32 tile that a cluster's pairs exchange)
-  uint8_t* staging = g.single ? smem + (g.cpairs > 1 ? BN * kHalf * 4 : 0) : smem + S * kStage;
+  uint8_t* staging = g.single ? smem : smem + S * kStage;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRegion);
   uint64_t* full = bars;              // [S] (leader) both CTAs' halves landed
   uint64_t* empty = full + kMaxStages;  // [S] the pair's MMAs have read the stage
@@ -309,6 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();   // both CTAs' barriers exist before either signals the other's
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (before the wait: its divisions are 0.5 us of the first load's way)
+  Item first{};
+  if (warp == 0) first = item_of(g, pair, kchunks);
   if (!g.late_wait) grid_dep_wait();
   grid_dep_launch();
   // (a wait gives up after 2 s: no CTA can have recorded one yet)
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const uint32_t fb0 = cluster_addr(smem_u32(full), crank & ~1u), base = smem_u32(smem);
       for (unsigned w = pair; ok && w < items; w += npairs) {
-        const Item q = item_of(g, w, kchunks);
+        const Item q = w == pair ? first : item_of(g, w, kchunks);
         const int32_t m0 = (int32_t)(q.mt * (2 * kHalf) + rank * kHalf);
         const int32_t n0 = (int32_t)(q.nt * BN + rank * kBHalf);
         for (int kc = q.k0; kc < q.k1; ++kc, at.next()) {
@@ -393,36 +398,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = split ? 32 : 64;                   // columns in 128 bytes
     const uint32_t acc_empty_leader = cluster_addr(smem_u32(&acc_empty[0]), crank & ~1u);
     Drain d(g, staging + grp * 2 * kOutBytes, bias_of[grp], smem_u32(&res_full[grp]), grp, r);
-    Place acc(2);
     // (a thread whose wait ran out goes on without waiting, so that its group's barriers
     // stay matched; the error header says that the values are not to be used)
-    for (unsigned w = pair; w < items; w += npairs, acc.next()) {
+    if (g.cpairs > 1) {
+      // One tile; the half of its columns that this pair finishes, a chunk of 64 a group
+      // (128 wide: of the first one alone).
+      constexpr int kCols = BN / 2;
+      const Item q = item_of(g, pair, kchunks);
+      const int64_t row0 = (int64_t)q.mt * (2 * kHalf) + rank * kHalf, n0 = (int64_t)q.nt * BN;
+      const int own = (int)(crank >> 1) * kCols + grp * 64, theirs = (int)(~crank >> 1 & 1) * kCols;
+      const int64_t col = n0 + own;
+      const bool rows = row0 < g.M, mine = rows && grp * 64 < kCols && col < g.N;
+      const uint32_t tbase = tmem + ((uint32_t)(lg * 32) << 16);
+      // 4 columns of all rows after one another, so that rows are 16 bytes apart
+      const float4* joined = reinterpret_cast<float4*>(smem + kRegion - joined_bytes(BN)) + r;
+      if (mine) d.load_bias(0, col);
+      d.ok = mbar_wait(smem_u32(&acc_full[0]), 0, g.err, 84);
+      tc_fence_after();
+      if (mine) d.open(tm_res, col, row0);
+      if (rows) {
+        const uint32_t to = cluster_addr(smem_u32(joined), crank ^ 2u);
+        for (int c = grp * (kCols / 2); c < (grp + 1) * (kCols / 2); c += 32) {
+          uint32_t v[32];
+          tmem_ld16(tbase + theirs + c, *reinterpret_cast<uint32_t(*)[16]>(v));
+          tmem_ld16(tbase + theirs + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            st_cluster4(to + (uint32_t)((c / 4 + i) * kHalf * 16), v[4 * i], v[4 * i + 1],
+                        v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      cluster_sync();   // (warps 0 and 1 come to it below)
+      if (mine) {
+        uint32_t v[64];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          tmem_ld16(tbase + own + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(v + 16 * i));
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 f = joined[(grp * 16 + i) * kHalf];
+          const float o[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[4 * i + k] = __float_as_uint(__uint_as_float(v[4 * i + k]) + o[k]);
+        }
+        d.finish(tm_out, tm_pre, v, col, row0, 0);
+      }
+      d.close();
+    }
+    Place acc(2);
+    for (unsigned w = pair; g.cpairs == 1 && w < items; w += npairs, acc.next()) {
       const Item q = item_of(g, w, kchunks);
       const int b = acc.s;
       const int64_t row0 = (int64_t)q.mt * (2 * kHalf) + rank * kHalf, n0 = (int64_t)q.nt * BN;
       const bool rows = row0 < g.M;
       const uint32_t tbase = tmem + ((uint32_t)(lg * 32) << 16) + (uint32_t)(b * 256);
       bool waited = false;
-      if (g.cpairs > 1) {
-        // the whole float32 tile into the ring's place (its MMAs are complete): 4 columns
-        // of all rows after one another, so that rows are 16 bytes apart
-        d.ok = d.ok && mbar_wait(smem_u32(&acc_full[b]), acc.parity, g.err, 84);
-        waited = true;
-        tc_fence_after();
-        float4* tile = reinterpret_cast<float4*>(smem) + r;
-        for (int c = grp * (BN / 2); c < (grp + 1) * (BN / 2); c += 32) {
-          uint32_t v[32];
-          tmem_ld16(tbase + c, *reinterpret_cast<uint32_t(*)[16]>(v));
-          tmem_ld16(tbase + c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            tile[(c / 4 + i) * kHalf] =
-                make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                            __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
-        }
-        break;   // one tile per cluster; it is finished below
-      }
       if (!split) d.load_bias(b, n0 + grp * 64);
       for (int c = grp * cw; rows && c < BN && n0 + c < g.N; c += 2 * cw) {
         const int64_t col = n0 + c;
@@ -452,42 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (g.cpairs == 1) d.close();
   }
-  if (g.cpairs > 1) {
-    tc_fence_before();
-    cluster_sync();   // the cluster's tiles are all there
-    if (warp >= 2) {
-      const int grp = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;
-      Drain d(g, staging + grp * 2 * kOutBytes, bias_of[grp], smem_u32(&res_full[grp]), grp, r);
-      const Item q = item_of(g, pair, kchunks);
-      const int64_t row0 = (int64_t)q.mt * (2 * kHalf) + rank * kHalf;
-      // this pair's columns: BN / cpairs of them, 64 at a time
-      const int cols = BN / g.cpairs, c0 = (int)(crank >> 1) * cols;
-      for (int c = c0 + grp * 64; c < c0 + cols; c += 128) {
-        const int64_t col = (int64_t)q.nt * BN + c;
-        if (row0 >= g.M || col >= g.N) break;
-        d.load_bias(0, col);
-        d.open(tm_res, col, row0);
-        uint32_t v[64];
-        const uint32_t at = smem_u32(smem) + (uint32_t)((c / 4) * kHalf + r) * 16;
-        for (int p = 0; p < g.cpairs; ++p) {
-          const uint32_t from = cluster_addr(at, 2 * p + rank);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float4 f = ld_cluster4(from + i * kHalf * 16);
-            const float o[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              v[4 * i + k] = __float_as_uint(p ? __uint_as_float(v[4 * i + k]) + o[k] : o[k]);
-          }
-        }
-        d.finish(tm_out, tm_pre, v, col, row0, 0);
-      }
-      d.close();
-    }
+  if (g.cpairs > 1 && warp < 2) {
+    __syncwarp();
+    cluster_sync();   // the cluster's halves are there
   }
   if (g.late_wait) grid_dep_wait();
   tc_fence_before();
-  cluster_sync();   // no CTA leaves while another may still signal it or read its tile
+  cluster_sync_relaxed();   // no CTA leaves while another may still signal it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
@@ -623,10 +627,11 @@ struct Cut {
 };
 
 // Estimated microseconds: waves of work items on 74 pairs (a 64-wide chunk of a 256 x
-// 256 tile takes a pair 0.28 us, of a 256 x 128 tile 0.16); 2.5 or 3.5 us for a cluster's
-// exchange; for splits the partial tiles' round trip through L2 and one launch.  (Clusters of
-// 4 pairs took 7.5 us more than no exchange, more than splits: 600 x 2048 x 512 in 14.1 us,
-// with 4 splits in 8.6.  256 x 8192 x 4096: two pairs 21.3 us, two splits 23.2.)
+// 256 tile takes a pair 0.28 us, of a 256 x 128 tile 0.16); 1 us for a cluster's
+// exchange; for splits the partial tiles' round trip through L2 and one launch.  Measured:
+// 256 x 8192 x 4096 two pairs 20 us, two splits 23; 530 x 5496 x 2208 one wave of two pairs a
+// 256 x 256 tile 23.5 us, of uncut 256 x 128 tiles 28.7; 600 x 2048 x 512 two pairs
+// 7.3 us, 4 splits 8.0, uncut 9.2.  (Tiles of 4 pairs took 6 us more than their splits.)
 Cut choose_cut(int64_t M, int64_t N, int64_t K) {
   const int64_t chunks = (K + kK - 1) / kK;
   Cut best{256, 1, 1};
@@ -639,7 +644,7 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K) {
       const double us = (double)(waves * ((chunks + s - 1) / s)) * (bn == 256 ? 0.28 : 0.16);
       // (a B200 holds 33 clusters of 4 CTAs with one CTA an SM)
       if (s == 1 || (s == 2 && tiles <= 33)) {
-        const double c = us + (s == 1 ? 0.0 : bn == 256 ? 3.5 : 2.5);
+        const double c = us + (s == 1 ? 0.0 : 1.0);
         if (c < best_us * 0.999) {
           best_us = c;
           best = {bn, s, 1};

@@ -274,6 +274,13 @@ __device__ __forceinline__ void cluster_sync() {
                ::: "memory");
 }
 
+// The same without waiting for this thread's earlier writes: where nothing that was written
+// is handed over.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+
 // Address of the same shared-memory offset in the leader CTA (rank 0).
 __device__ __forceinline__ uint32_t leader_addr(uint32_t saddr) {
   uint32_t r;
@@ -296,6 +303,13 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t cluster_addr) {
                : "r"(cluster_addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ void st_cluster4(uint32_t cluster_addr, uint32_t x, uint32_t y,
+                                            uint32_t z, uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(x),
+               "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 
 // Arrive on an mbarrier given by its shared::cluster address (another CTA's).
