@@ -10,8 +10,9 @@
 //
 // A cluster of C CTAs shares a tile of 128 features, each a range of the contracted
 // index, so that few tiles still fill the GPU; their float32 tiles meet in shared memory
-// (no round trip through global memory, no second kernel): each CTA reads its share of
-// the columns from the others in rank order, so two runs give the same bits.
+// (no round trip through global memory, no second kernel): each CTA writes to the others
+// what they finish and adds what it got in rank order, so two runs give the same bits.
+// (Left for the others to read: 8 x 4096 -> 1024 6.6 us instead of 5.3.)
 #include <cuda.h>
 
 #include "block_epilogue.cuh"
@@ -152,51 +153,55 @@ __global__ void __launch_bounds__(kThreads)
       if (ok) umma_commit(smem_u32(&done));
     }
   }
-  // The tile [T][128] into the ring's place: all its loads were consumed by the MMAs.
-  float* tile = reinterpret_cast<float*>(smem);
+  // CTA q of the cluster finishes F features of all rows; the others write theirs of them,
+  // float32, to its shared memory, [CTA][row][feature], in the ring's place: once the MMAs of
+  // all have consumed their rings.
+  const int F = kTile / (int)C;
   if (warp >= 2) {
     const int lg = warp & 3, et = lg * 32 + lane;   // TMEM lane = feature of the tile
-    if (mbar_wait(smem_u32(&done), 0, g.err, 103)) {
-      tc_fence_after();
-      const uint32_t tb = tmem + ((uint32_t)(lg * 32) << 16);
-      for (int c = 0; c < g.T; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(tb + (uint32_t)c, r);
-        tmem_ld_wait();
-        // (the tile's place holds whole blocks of 16 rows)
+    const bool ok = mbar_wait(smem_u32(&done), 0, g.err, 103);
+    __syncwarp();
+    cluster_arrive();
+    tc_fence_after();
+    const uint32_t tb = tmem + ((uint32_t)(lg * 32) << 16);
+    const uint32_t to = cluster_addr(base, (uint32_t)(et / F)) +
+                        ((uint32_t)((int)rank * g.nb * F) + (uint32_t)(et % F)) * 4;
+    for (int c = 0; c < g.nb; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(tb + (uint32_t)c, r);
+      tmem_ld_wait();
+      if (c == 0) cluster_wait();
+      if (ok) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) tile[(c + i) * kTile + et] = __uint_as_float(r[i]);
+        for (int i = 0; i < 16; ++i) st_cluster(to + (uint32_t)((c + i) * F) * 4, r[i]);
       }
     }
-    tc_fence_before();
+  } else {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
   }
-  __syncthreads();
+  tc_fence_before();
   cluster_sync();
-  // this CTA's share of the (row, 8 features) items
-  const unsigned items = (unsigned)g.T * (kTile / 8), i1 = items * (rank + 1) / C;
-  for (unsigned i = items * rank / C + tid; i < i1; i += kThreads) {
-    const unsigned t = i / (kTile / 8), f = i % (kTile / 8) * 8;
-    const int64_t col = n0 + f;
+  // in rank order, 8 features of a row at a time
+  const float* parts = reinterpret_cast<const float*>(smem);
+  const int f8 = F / 8, items = g.T * f8;
+  for (int i = tid; i < items; i += kThreads) {
+    const int t = i / f8, f = (i - t * f8) * 8;
+    const int64_t col = n0 + rank * F + f;
     if (col >= g.N) continue;
-    const uint32_t at = base + (t * kTile + f) * 4;
-    const float4 l0 = *reinterpret_cast<const float4*>(tile + t * kTile + f);
-    const float4 l1 = *reinterpret_cast<const float4*>(tile + t * kTile + f + 4);
-    float v[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
-    if (C > 1) {   // in rank order
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    }
+    const float* p = parts + t * F + f;
+    float v[8] = {};
 #pragma unroll 4
-    for (uint32_t q = 0; C > 1 && q < C; ++q) {
-      const uint32_t p = cluster_addr(at, q);
-      const float4 a = ld_cluster4(p), b = ld_cluster4(p + 16);
+    for (uint32_t q = 0; q < C; ++q, p += g.nb * F) {
+      const float4 a = *reinterpret_cast<const float4*>(p);
+      const float4 b = *reinterpret_cast<const float4*>(p + 4);
       v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
     }
     finish8(g.ep, v, (int64_t)t * g.N + col, col);
   }
   if (g.late_wait) grid_dep_wait();
-  cluster_sync();   // no CTA leaves while another may read its tile
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, g.tmem_cols);
@@ -227,9 +232,12 @@ struct FewShape {
 
 // The least estimated time over cluster sizes and one or two CTAs an SM (two hide each
 // other's start and end and let up to 296 CTAs stream at once, with rings of half the
-// size).  An SM's rate for weights is what its rings hold over 1.2 us, a load's latency
-// from HBM under load; what passes through the SM, rows included, goes at 0.11 MB/us at
-// most; a wave of CTAs starts and ends in about 3 us, a cluster's two meetings in 1 to 2.
+// size).  What passes through an SM, rows included, goes at 0.095 MB/us at most; the stream
+// from HBM at 6.9 MB/us with 1.8 MB on their way at least, and slower with few SMs at it; a
+// wave of CTAs starts and ends in 3.2 us; what a cluster's CTAs write to each other grows with
+// the rows and the CTAs.  Measured, us: 16 x 8192 -> 8192 with clusters of 1, 2 and 4 CTAs,
+// one an SM, 28.1, 22.9, 25.6 (two rounds), two an SM 31.8, 25.9, 21.7; 1 x 1024 -> 1024 6.3,
+// 4.9, 4.2 and of 8 CTAs 3.8; 100 x 4096 -> 4096 18.6, 12.6, 10.7, 22.7 (three rounds).
 FewShape few_shape(int64_t T, int64_t N, int64_t K) {
   // clusters of 1, 2, 4 and 8 CTAs that a B200 holds, with one or two CTAs an SM
   static const int kClusters[2][9] = {{0, 148, 74, 0, 33, 0, 0, 0, 15},
@@ -238,7 +246,7 @@ FewShape few_shape(int64_t T, int64_t N, int64_t K) {
   f.nb = (int)(ceil_div(T, 16) * 16);
   const int64_t tiles = ceil_div(N, kTile), chunks = ceil_div(K, kK);
   const size_t stage = kWBytes + (size_t)f.nb * 128, tile = (size_t)f.nb * kTile * 4;
-  const double hbm = (double)N * (double)K * 2.0 / 6.5e6;
+  const double hbm = (double)N * (double)K * 2.0 / 6.9e6;
   double best = 1e30;
   for (int c = 1; c <= kMaxCluster; c *= 2) {
     if (c > 1 && chunks / c < 2) break;
@@ -249,14 +257,16 @@ FewShape few_shape(int64_t T, int64_t N, int64_t K) {
       if (stages < 3 || tile > most) break;
       if (stages > kMaxStages) stages = kMaxStages;
       if (stages > steps) stages = steps;
-      const int64_t waves = ceil_div(tiles, kClusters[per - 1][c]);
+      const int64_t held = kClusters[per - 1][c], waves = ceil_div(tiles, held);
+      const int64_t at_once = ctas < held * c ? ctas : held * c;
       const int64_t on_sm = ctas < 148 * per ? ceil_div(ctas, 148) : per;
-      const double latency = (double)steps / (double)stages * 1.2;
-      const double through = (double)(on_sm * steps) * (double)stage / 0.11e6;
-      double us = (double)waves * (latency > through ? latency : through);
-      if (us < hbm) us = hbm;
-      us += 3.0 * (double)waves + (c > 1 ? 1.0 + 0.1 * c : 0.0);
-      if (us < best * 0.98) {
+      const double through = (double)(waves * on_sm * steps) * (double)stage / 0.095e6;
+      double us = hbm * (1.0 + 1.8e6 / ((double)(at_once * stages) * (double)kWBytes));
+      if (at_once < 148) us *= 1.2 - 0.2 * (double)at_once / 148.0;
+      if (us < through) us = through;
+      us += 3.2 * (double)waves;
+      if (c > 1) us += (double)c * (0.02 + 0.0055 * (double)(f.nb - 16));
+      if (us < best * 0.995) {
         best = us;
         f.cluster = c;
         f.stages = (int)stages;

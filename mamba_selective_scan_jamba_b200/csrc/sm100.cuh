@@ -274,7 +274,15 @@ __device__ __forceinline__ void cluster_sync() {
                ::: "memory");
 }
 
-// The same without waiting for this thread's earlier writes: where nothing that was written
+// Its two halves.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Both without waiting for this thread's earlier writes: where nothing that was written
 // is handed over.
 __device__ __forceinline__ void cluster_sync_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
@@ -295,14 +303,9 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
   return r;
 }
 
-// 16 bytes of another CTA's shared memory.
-__device__ __forceinline__ float4 ld_cluster4(uint32_t cluster_addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr)
-               : "memory");
-  return v;
+// To another CTA's shared memory.
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t x) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(x) : "memory");
 }
 
 __device__ __forceinline__ void st_cluster4(uint32_t cluster_addr, uint32_t x, uint32_t y,
