@@ -309,12 +309,18 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& x, const FewArgs
 
 }  // namespace
 
-// Up to 64 rows, or 128 over a contracted index above 1024: a tile's exchange grows with the
+// Up to 64 rows, and up to 192 over a long contracted index: a tile's exchange grows with the
 // rows, k_linear_pair's does not, but its 256-row tiles read the weights no faster for few
-// rows.  128 rows: 8192 -> 4096 18.8 us here, 20.8 us there; 1024 -> 1024 8.0 us here, 6.6 us
-// there; 160 rows: 8192 -> 4096 20.9 us both, 1024 -> 1024 9.5 us here, 6.6 us there.
+// rows.  Microseconds here and there: 96 rows, 512 -> 4096 6.2, 5.5; 1024 -> 4096 7.0, 7.2;
+// 128 rows, 1024 -> 1024 6.6, 6.2; 8192 -> 4096 15.8, 19.2; 160 rows, 2048 -> 4096 9.3, 8.9;
+// 4096 -> 8192 17.5, 20.1; 192 rows, 4096 -> 1024 10.4, 9.1; 8192 -> 4096 18.5, 19.6; 256
+// rows, 8192 -> 4096 21.9, 19.8.
 bool linear_few(int64_t rows, int64_t contracted) {
-  return rows <= 64 || (rows <= 128 && contracted > 1024);
+  const int64_t most = contracted <= 1024   ? 64
+                       : contracted < 4096 ? 128
+                       : contracted < 8192 ? 160
+                                           : 192;
+  return rows <= most;
 }
 
 cudaError_t run_linear_few(int64_t T, int64_t N, int64_t K, const void* x, const void* w, bool w_mn,

@@ -276,3 +276,23 @@ def test_linear_gradient_against_differences():
         # each entry is within about 3 half steps of its magnitude; signs are random
         mag = sum((q.double() * v).square().sum() for q, v in parts).sqrt()
         assert abs(num - ana) <= 8 * HALF * mag
+
+
+# few rows over long contracted indexes, with each size of a cluster; two pairs on a tile,
+# both widths, and a last row tile whose second half is empty
+JOINED = [(1, 1024, 1024), (2, 16384, 136), (8, 4096, 1024), (40, 6000, 3000), (64, 520, 512),
+          (100, 4104, 1000), (150, 4096, 8192), (160, 4104, 264), (192, 8192, 520),
+          (300, 2048, 1304), (390, 5256, 2008), (530, 5496, 2208), (818, 4200, 1440),
+          (2619, 1048, 96)]
+
+
+@pytest.mark.parametrize("m,k,n", JOINED)
+def test_linear_products_joined_in_shared_memory(m, k, n):
+    import torch
+    i = m % 4
+    t = make(m, k, n, seed=m + 2 * n)
+    out, pre = check_fwd(t, ACTS[i], bias=i % 2 == 0, residual=True)
+    again, _ = run_fwd(t, ACTS[i], bias=i % 2 == 0, residual=True)
+    assert torch.equal(out, again)
+    check_fwd(t, "none", bias=False, residual=False)
+    check_bwd(t, ACTS[i], pre)
