@@ -306,6 +306,29 @@ def _bad(msg: str):
     raise JmixError(JM_ERR_INVALID_ARG, msg)
 
 
+def _check_rows(name, t, d) -> None:
+    """The rows of t, all dimensions but the last, have to lie d.x_stride values apart: a 3-D
+    slice or a transposed tensor has no such pitch, and its address does not say so.  (Where
+    t and the dims' rows are both packed, t may be grouped otherwise; a tensor of one
+    dimension is memory without rows of its own.)"""
+    if t.is_contiguous() and (d.x_stride == d.cols or t.dim() < 2):
+        return
+    if t.dim() < 2 or t.shape[-1] > 1 and t.stride(-1) != 1:
+        _bad(f"{name} is not contiguous")
+    if t.shape[-1] < d.cols:
+        _bad(f"{name} has rows of {t.shape[-1]} values, the dims say {d.cols}")
+    pitch = end = None   # of the rows so far, and where the next dimension's would go on
+    for n, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if pitch is not None and step != end:
+            _bad(f"{name} is not contiguous: its rows of shape {tuple(t.shape)} do not lie at "
+                 "one stride")
+        pitch, end = step if pitch is None else pitch, step * n
+    if pitch is not None and pitch != d.x_stride and d.rows > 1:
+        _bad(f"{name} has row stride {pitch}, the dims say {d.x_stride}")
+
+
 def _call(fn, d, spec, tensors, tail=(), stream=None, check: bool = True) -> int:
     """fn(d, addresses of `tensors`, *tail, stream).  A tensor's layout, type and device
     cannot be read from its address, so they are checked here against `spec`, a tuple of
@@ -319,11 +342,10 @@ def _call(fn, d, spec, tensors, tail=(), stream=None, check: bool = True) -> int
             continue
         if kind != _RAW and t.dtype is not types[kind]:
             _bad(f"{name} is {t.dtype}, the call needs {types[kind]}")
-        if not t.is_contiguous():
-            if kind != _ROWS or t.shape[-1] > 1 and t.stride(-1) != 1:
-                _bad(f"{name} is not contiguous")
-            if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != d.x_stride:
-                _bad(f"{name} has row stride {t.stride(0)}, the dims say {d.x_stride}")
+        if kind == _ROWS:
+            _check_rows(name, t, d)
+        elif not t.is_contiguous():
+            _bad(f"{name} is not contiguous")
         at = t.get_device()
         if at != dev or at < 0:
             if at >= 0 and dev < 0:

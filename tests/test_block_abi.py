@@ -110,6 +110,54 @@ def test_binding_checks_tensors():
         jmix.jm_norm_fwd(jmix.norm_dims(4, 32), t, F, F, stream=0)
 
 
+def rows_verdict(x, rows, cols, x_stride=None):
+    """What the binding says of x before it asks for its device (these tensors have no GPU's
+    address, so that an accepted one ends there)."""
+    d = jmix.norm_dims(rows, cols, x_stride=x_stride)
+    said = []
+    for call in (lambda: jmix.jm_norm_fwd(d, x, F, F, stream=0),
+                 lambda: jmix.jm_norm_bwd(d, F, x, F, F, F, W, 1 << 30, stream=0)):
+        with pytest.raises(jmix.JmixError) as e:
+            call()
+        assert e.value.status == jmix.JM_ERR_INVALID_ARG
+        said.append("ok" if "CUDA device" in str(e.value) else str(e.value))
+    assert said[0] == said[1]
+    return said[0]
+
+
+def test_binding_checks_the_row_pitch():
+    import torch
+    x = torch.zeros(4, 6, 32, dtype=torch.bfloat16)
+    wide = torch.zeros(24, 64, dtype=torch.bfloat16)
+    # one pitch, and the dims say it
+    assert rows_verdict(x, 24, 32) == "ok"
+    assert rows_verdict(x, 4, 192) == "ok"                       # packed, grouped otherwise
+    assert rows_verdict(x.view(-1), 24, 32) == "ok"
+    assert rows_verdict(wide[:, :32], 24, 32, 64) == "ok"
+    assert rows_verdict(wide, 24, 32, 64) == "ok"                # the rows' first 32 values
+    assert rows_verdict(wide.view(4, 6, 64)[..., :32], 24, 32, 64) == "ok"
+    assert rows_verdict(x[:, 0], 4, 32, 192) == "ok"
+    assert rows_verdict(x[:, :1], 4, 32, 192) == "ok"
+    assert rows_verdict(wide[:1, :32], 1, 32, 40) == "ok"        # one row has no pitch
+    assert rows_verdict(wide[:, :1], 24, 1, 64) == "ok"
+    # packed tensors and other strides in the dims
+    assert "row stride 32, the dims say 64" in rows_verdict(x.view(24, 32), 24, 32, 64)
+    assert "row stride 32, the dims say 40" in rows_verdict(x, 24, 32, 40)
+    assert "row stride 64, the dims say 32" in rows_verdict(wide[:, :32], 24, 32)
+    # more than two dimensions: a slice of the columns, every other one, transposed
+    assert "row stride 64, the dims say 32" in rows_verdict(wide.view(4, 6, 64)[..., :32], 24, 32)
+    assert "one stride" in rows_verdict(x[::2], 12, 32)
+    assert "one stride" in rows_verdict(x.transpose(0, 1), 24, 32)
+    assert "one stride" in rows_verdict(x[:, :3], 12, 32)
+    # a gap between the values of a row, rows shorter than the dims say
+    assert "not contiguous" in rows_verdict(wide[:, ::2], 24, 32, 64)
+    assert "not contiguous" in rows_verdict(x.transpose(1, 2), 128, 6)
+    assert "not contiguous" in rows_verdict(wide.view(-1)[::2], 24, 32)
+    assert "rows of 16" in rows_verdict(wide[:, :16], 24, 32, 64)
+    assert "row stride 0" in rows_verdict(x[0, :1].expand(24, 32), 24, 32)
+    assert "row stride 0" in rows_verdict(x[0, 0].expand(4, 6, 32), 24, 32)
+
+
 def linear_fwd(d, nbytes=None, **over):
     a = dict(x=F, w=F + G, out=F + 2 * G, workspace=W,
              ws_bytes=jmix.jm_linear_fwd_workspace_size(d) if nbytes is None else nbytes)
