@@ -312,6 +312,9 @@ def _check_rows(name, t, d) -> None:
     t and the dims' rows are both packed, t may be grouped otherwise; a tensor of one
     dimension is memory without rows of its own.)"""
     if t.is_contiguous() and (d.x_stride == d.cols or t.dim() < 2):
+        need = (d.rows - 1) * d.x_stride + d.cols if d.rows > 0 else 0
+        if t.numel() < need:
+            _bad(f"{name} has {t.numel()} values, the call needs {need}")
         return
     if t.dim() < 2 or t.shape[-1] > 1 and t.stride(-1) != 1:
         _bad(f"{name} is not contiguous")
@@ -327,16 +330,19 @@ def _check_rows(name, t, d) -> None:
         pitch, end = step if pitch is None else pitch, step * n
     if pitch is not None and pitch != d.x_stride and d.rows > 1:
         _bad(f"{name} has row stride {pitch}, the dims say {d.x_stride}")
+    if t.numel() < d.rows * t.shape[-1]:
+        _bad(f"{name} has {t.numel() // t.shape[-1]} rows, the dims say {d.rows}")
 
 
-def _call(fn, d, spec, tensors, tail=(), stream=None, check: bool = True) -> int:
-    """fn(d, addresses of `tensors`, *tail, stream).  A tensor's layout, type and device
+def _call(fn, d, spec, needs, tensors, tail=(), stream=None, check: bool = True) -> int:
+    """fn(d, addresses of `tensors`, *tail, stream).  A tensor's layout, type, size and device
     cannot be read from its address, so they are checked here against `spec`, a tuple of
-    (name, kind).  (A decode step's operators take microseconds: this path is kept short.)"""
+    (name, kind), and `needs`, the values (of the workspace: bytes) the call reads or writes
+    there.  (A decode step's operators take microseconds: this path is kept short.)"""
     if _types is None:
         _use_torch()
     types, dev, args = _types.get(d.io, _types[JM_BF16]), -1, []
-    for (name, kind), t in zip(spec, tensors):
+    for (name, kind), need, t in zip(spec, needs, tensors):
         if t is None or type(t) is int:
             args.append(t)
             continue
@@ -346,6 +352,9 @@ def _call(fn, d, spec, tensors, tail=(), stream=None, check: bool = True) -> int
             _check_rows(name, t, d)
         elif not t.is_contiguous():
             _bad(f"{name} is not contiguous")
+        has = t.nbytes if kind == _RAW else t.numel()
+        if has < need:
+            _bad(f"{name} has {has} {'bytes' if kind == _RAW else 'values'}, the call needs {need}")
         at = t.get_device()
         if at != dev or at < 0:
             if at >= 0 and dev < 0:
@@ -383,7 +392,9 @@ _MOE_FWD = _spec("x router_w w_gate w_up w_down residual out topk_idx topk_w wor
 def jm_norm_fwd(d: jm_norm_dims, x, weight, y, bias=None, residual=None, sum_out=None, stats=None,
                 stream=None, check: bool = True) -> int:
     """Residual add and LayerNorm / RMSNorm of each row (see include/jmix.h)."""
-    return _call(load().jm_norm_fwd, d, _NORM_FWD,
+    rows, c = d.rows, d.cols
+    n = rows * c
+    return _call(load().jm_norm_fwd, d, _NORM_FWD, (n, n, c, c, n, n, 2 * rows),
                  (x, residual, weight, bias, y, sum_out, stats), (), stream, check)
 
 
@@ -394,7 +405,9 @@ def jm_norm_bwd_workspace_size(d: jm_norm_dims) -> int:
 def jm_norm_bwd(d: jm_norm_dims, g_y, x, weight, stats, g_x, workspace, ws_bytes: int, g_sum=None,
                 g_weight=None, g_bias=None, stream=None, check: bool = True) -> int:
     """Backward of jm_norm_fwd (see include/jmix.h); x is the forward's sum, or its x."""
-    return _call(load().jm_norm_bwd, d, _NORM_BWD,
+    rows, c = d.rows, d.cols
+    n = rows * c
+    return _call(load().jm_norm_bwd, d, _NORM_BWD, (n, n, c, 2 * rows, n, n, c, c, ws_bytes),
                  (g_y, x, weight, stats, g_sum, g_x, g_weight, g_bias, workspace), (ws_bytes,),
                  stream, check)
 
@@ -406,7 +419,9 @@ def jm_linear_fwd_workspace_size(d: jm_linear_dims) -> int:
 def jm_linear_fwd(d: jm_linear_dims, x, w, out, workspace, ws_bytes: int, bias=None, residual=None,
                   pre=None, stream=None, check: bool = True) -> int:
     """out = act(x . w^T + bias) + residual (see include/jmix.h)."""
+    m, k, n = d.rows, d.in_features, d.out_features
     return _call(load().jm_linear_fwd, d, _LINEAR_FWD,
+                 (m * k, n * k, n, m * n, m * n, m * n, ws_bytes),
                  (x, w, bias, residual, out, pre, workspace), (ws_bytes,), stream, check)
 
 
@@ -417,7 +432,9 @@ def jm_linear_bwd_workspace_size(d: jm_linear_dims) -> int:
 def jm_linear_bwd(d: jm_linear_dims, g_out, x, w, workspace, ws_bytes: int, pre=None, g_x=None,
                   g_w=None, g_bias=None, stream=None, check: bool = True) -> int:
     """Backward of jm_linear_fwd (see include/jmix.h)."""
+    m, k, n = d.rows, d.in_features, d.out_features
     return _call(load().jm_linear_bwd, d, _LINEAR_BWD,
+                 (m * n, m * k, n * k, m * n, m * k, n * k, n, ws_bytes),
                  (g_out, x, w, pre, g_x, g_w, g_bias, workspace), (ws_bytes,), stream, check)
 
 
@@ -428,7 +445,10 @@ def jm_moe_fwd_workspace_size(d: jm_moe_dims) -> int:
 def jm_moe_fwd(d: jm_moe_dims, x, router_w, w_gate, w_up, w_down, out, workspace, ws_bytes: int,
                residual=None, topk_idx=None, topk_w=None, stream=None, check: bool = True) -> int:
     """Mixture-of-experts layer for few tokens (see include/jmix.h)."""
+    td, pairs, e = d.tokens * d.d_model, d.tokens * d.top_k, d.n_experts
+    w = e * d.d_ff * d.d_model
     return _call(load().jm_moe_fwd, d, _MOE_FWD,
+                 (td, e * d.d_model, w, w, w, td, td, pairs, pairs, ws_bytes),
                  (x, router_w, w_gate, w_up, w_down, residual, out, topk_idx, topk_w, workspace),
                  (ws_bytes,), stream, check)
 

@@ -158,6 +158,52 @@ def test_binding_checks_the_row_pitch():
     assert "row stride 0" in rows_verdict(x[0, 0].expand(4, 6, 32), 24, 32)
 
 
+def test_binding_checks_the_number_of_values_of_x():
+    import torch
+    x = torch.zeros(24, 32, dtype=torch.bfloat16)
+    assert "768 values, the call needs 800" in rows_verdict(x, 25, 32)
+    assert rows_verdict(x, 23, 32) == "ok"                       # a buffer for more rows
+    assert "768 values, the call needs 1504" in rows_verdict(x.view(-1), 24, 32, 64)
+    assert rows_verdict(x.view(-1), 12, 32, 64) == "ok"
+    assert "24 rows, the dims say 25" in rows_verdict(torch.zeros(24, 64, dtype=torch.bfloat16)[:, :32],
+                                                      25, 32, 64)
+    assert "24 rows, the dims say 25" in rows_verdict(x, 25, 16, 32)
+
+
+NORM, LINEAR, MOE = (jmix.norm_dims(6, 40, kind=jmix.JM_NORM_LAYER), jmix.linear_dims(6, 40, 56, 1),
+                     jmix.moe_dims(6, 40, 56, 5, 2))
+SIZED = [  # call, dims, {argument: values the call reads or writes}
+    ("jm_norm_fwd", NORM, dict(weight=40, y=240, bias=40, residual=240, sum_out=240, stats=12)),
+    ("jm_norm_bwd", NORM, dict(g_y=240, weight=40, stats=12, g_x=240, g_sum=240, g_weight=40,
+                               g_bias=40, workspace=1024)),
+    ("jm_linear_fwd", LINEAR, dict(x=240, w=2240, out=336, bias=56, residual=336, pre=336,
+                                   workspace=1024)),
+    ("jm_linear_bwd", LINEAR, dict(g_out=336, x=240, w=2240, pre=336, g_x=240, g_w=2240, g_bias=56,
+                                   workspace=1024)),
+    ("jm_moe_fwd", MOE, dict(x=240, router_w=200, w_gate=11200, w_up=11200, w_down=11200, out=240,
+                             residual=240, topk_idx=12, topk_w=12, workspace=1024)),
+]
+
+
+@pytest.mark.parametrize("call,d,needs", SIZED)
+def test_binding_checks_the_number_of_values(call, d, needs):
+    """A tensor with fewer values than the dims say is refused, one with more is not."""
+    import torch
+    types = dict(stats=torch.float32, topk_w=torch.float32, topk_idx=torch.int32,
+                 workspace=torch.uint8)
+    base = dict(x=F) if "x" not in needs else {}
+    base.update({k: F for k in needs})
+    if "workspace" in needs:
+        base["ws_bytes"] = 1024
+    for k, n in needs.items():
+        for have, msg in ((n - 1, f"{k.replace('sum_out', 'sum')} has {n - 1} "), (n, "CUDA device"),
+                          (n + 8, "CUDA device")):
+            t = torch.zeros(have, dtype=types.get(k, torch.bfloat16))
+            with pytest.raises(jmix.JmixError, match=msg) as e:
+                getattr(jmix, call)(d, **{**base, k: t}, stream=0)
+            assert e.value.status == jmix.JM_ERR_INVALID_ARG
+
+
 def linear_fwd(d, nbytes=None, **over):
     a = dict(x=F, w=F + G, out=F + 2 * G, workspace=W,
              ws_bytes=jmix.jm_linear_fwd_workspace_size(d) if nbytes is None else nbytes)
