@@ -353,6 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // The stages' last signals come from the pair's leader and are waited for here, so that
+      // none is on its way to a CTA that has left.
+      for (int i = 0; ok && i < S; ++i, at.next())
+        ok = mbar_wait(smem_u32(&empty[at.s]), at.parity ^ 1u, g.err, 79);
     }
   } else if (warp == 1) {
     if (leader && elect_one()) {
@@ -368,7 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (unsigned w = pair; ok && w < items; w += npairs, acc.next()) {
         const Item q = item_of(g, w, kchunks);
         const int b = acc.s;
-        if (!mbar_wait(smem_u32(&acc_empty[b]), acc.parity ^ 1u, g.err, 82)) break;
+        if (!mbar_wait(smem_u32(&acc_empty[b]), acc.parity ^ 1u, g.err, 82)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t d_tmem = tmem + (uint32_t)(b * 256);
         for (int kc = q.k0; kc < q.k1; ++kc, at.next()) {
@@ -389,6 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) umma_commit_pair(smem_u32(&acc_full[b]), both);
       }
+      // The pair's other CTA signals acc_empty by arrives that nothing orders before the last
+      // cluster barrier: this CTA may not leave before those of its last two tiles are in.
+      // (A cluster that shares a tile never signals it.)
+      for (int i = 0; ok && g.cpairs == 1 && i < 2; ++i, acc.next())
+        ok = mbar_wait(smem_u32(&acc_empty[acc.s]), acc.parity ^ 1u, g.err, 78);
     }
   } else {
     // epilogue: this CTA's 128 rows of the pair's 256-row tile, a row per thread; two
@@ -491,7 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (g.late_wait) grid_dep_wait();
   tc_fence_before();
-  cluster_sync_relaxed();   // no CTA leaves while another may still signal it
+  // No CTA leaves while another may still signal it.  The barrier itself orders no signal;
+  // each is waited for by the CTA it goes to: full by the MMAs, acc_full by the epilogue,
+  // empty by the producer and acc_empty by the leader's MMA warp at their ends.
+  cluster_sync_relaxed();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);

@@ -296,3 +296,35 @@ def test_linear_products_joined_in_shared_memory(m, k, n):
     assert torch.equal(out, again)
     check_fwd(t, "none", bias=False, residual=False)
     check_bwd(t, ACTS[i], pre)
+
+
+# tiles a CTA pair: one to three of short and of long contracted indexes (fewer K chunks than
+# ring stages, and more), a last tile with an empty half or with fewer columns
+DRAINED = [(300, 64, 2048), (4096, 64, 2048), (9000, 72, 2056), (19000, 8, 520), (2305, 1032, 4104),
+           (5000, 1544, 2048), (10000, 1544, 264)]
+
+
+@pytest.mark.parametrize("m,k,n", DRAINED)
+def test_linear_pairs_end_with_every_signal_received(m, k, n):
+    """CTAs of one launch follow those of another on their SM at once: with a signal still on
+    its way to a CTA that has left, the next one's barriers would count it.  Every wait at the
+    kernel's end is satisfied (the error header says so) and all launches give the same bits."""
+    import torch
+    from mamba_selective_scan_jamba_b200 import devio, jmix
+    t = make(m, k, n, seed=m + k)
+    out, pre = run_fwd(t, "relu")
+    o = run_bwd(t, "relu", pre)
+    d = jmix.linear_dims(m, k, n, act=ACTS.index("relu"))
+    nf, nb = jmix.jm_linear_fwd_workspace_size(d), jmix.jm_linear_bwd_workspace_size(d)
+    wss = [devio.workspace(max(nf, nb)) for _ in range(16)]
+    outs = [(torch.empty_like(out), torch.empty_like(o["g_x"]), torch.empty_like(o["g_w"]))
+            for _ in range(2)]
+    for i, ws in enumerate(wss):
+        q = outs[i % 2]
+        jmix.jm_linear_fwd(d, t["x"], t["w"], q[0], ws, nf, bias=t["b"], residual=t["r"])
+        jmix.jm_linear_bwd(d, t["g"], t["x"], t["w"], ws, nb, pre=pre, g_x=q[1], g_w=q[2])
+    torch.cuda.synchronize()
+    for ws in wss:
+        assert jmix.jm_poll_error(ws) == jmix.JM_OK, jmix.jm_last_error()
+    for q in outs:
+        assert torch.equal(q[0], out) and torch.equal(q[1], o["g_x"]) and torch.equal(q[2], o["g_w"])
