@@ -297,6 +297,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                            (int32_t)(nt * kGN + rank * kPHalf));
         }
       }
+      // (the leader's signals that the last stages are read: none may be on its way to a CTA
+      // that has left)
+      for (int i = 0; ok && i < kPStages; ++i, ++it)
+        if (it >= kPStages)
+          ok = mbar_wait(smem_u32(&empty[it % kPStages]), (uint32_t)((it / kPStages) - 1) & 1u,
+                         g.err, 75);
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
