@@ -345,10 +345,11 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const MoeKArgs a) {
     for (unsigned i = threadIdx.x; i < sizeof(Sync) / 4; i += kRouteThreads) s[i] = 0u;
     if (threadIdx.x < sizeof(ErrFlags) / 4) reinterpret_cast<unsigned*>(a.err)[threadIdx.x] = 0u;
   }
-  // this CTA's experts rank, rank + ranks, ...; few of them are cut along D too
-  const int mine = (a.E - rank + ranks - 1) / ranks;
+  // this CTA's experts rank, rank + ranks, ...; few of them are cut along D too, alike in
+  // every CTA, so that equal rows of the router give equal logits
+  const int mine = (a.E - rank + ranks - 1) / ranks, most = (a.E + ranks - 1) / ranks;
   int cuts = 1;
-  while (mine * cuts * 2 <= kW) cuts *= 2;
+  while (most * cuts * 2 <= kW) cuts *= 2;
   const int n8 = a.D / 8;
   const uint4* xr = reinterpret_cast<const uint4*>(a.x) + (int64_t)t * n8;
   for (int j = warp; j < mine * cuts; j += kW) {

@@ -226,3 +226,19 @@ def test_moe_two_calls_on_two_streams():
     for o, r, w in zip(outs, refs, wss):
         assert torch.equal(o, r)
         assert jmix.jm_poll_error(w) == jmix.JM_OK
+
+
+@pytest.mark.parametrize("t", [1, 40])
+@pytest.mark.parametrize("e", [2, 3, 9, 17, 250])
+def test_moe_equal_experts_tie(t, e):
+    """Rows of the router that are alike give the same bits whichever CTA sums them, with
+    products of very different sizes, whose sum depends on its order."""
+    import torch
+    m = make(t, 4096, 64, e, seed=e)
+    size = torch.exp2(torch.randint(-40, 40, (4096,), generator=torch.Generator().manual_seed(e)))
+    m["x"] = (m["x"].float() * size.cuda()).to(torch.bfloat16)
+    m["wr"][:] = m["wr"][0]
+    k = min(e, 8)
+    _, idx, w = run(m, k, TOPK)
+    assert (idx == torch.arange(k, device="cuda")).all()
+    assert ((w - 1 / k).abs() <= 4 * E32).all()
