@@ -228,6 +228,39 @@ def test_moe_two_calls_on_two_streams():
         assert jmix.jm_poll_error(w) == jmix.JM_OK
 
 
+E64 = 2.0 ** -53
+
+
+@pytest.mark.parametrize("t,d,e,k", [(1, 4096, 16, 2), (40, 1024, 9, 3), (256, 4096, 16, 2),
+                                     (64, 264, 250, 8)])
+def test_moe_close_logits_keep_their_order(t, d, e, k):
+    """Logits that differ by less than a float32 sum of eight products resolves (a channel of
+    x is 30000 times the others) are put in order as float64 sums of d exact products, within
+    d + 16 roundings of sum|x w| here and d in the reference, tell them apart."""
+    import torch
+    m = make(t, d, 64, e, seed=t + e)
+    g = torch.Generator().manual_seed(e)
+    m["x"][:, 5] = 30000.0
+    m["wr"][:] = m["wr"][0]
+    m["wr"][:, 5] = 0.0078125
+    near = torch.randn(e, 8, generator=g) * 2.0 ** -10    # beside the large channel
+    near[:, 5] = 0.0078125
+    m["wr"][:, :8] = near.to(torch.bfloat16).cuda()
+    x = m["x"].double()
+    logits = x @ m["wr"].double().t()
+    mag = x.abs() @ m["wr"].double().abs().t().amax(1, keepdim=True)
+    val, want = torch.sort(logits, dim=1, descending=True, stable=True)
+    gap = val[:, :k] - val[:, 1:k + 1]
+    sure = (gap > (2 * d + 32) * E64 * mag).all(1)
+    assert sure.float().mean() >= 0.9 and (gap < 64 * E32 * mag).float().mean() >= 0.5
+    _, idx, w = run(m, k, TOPK)
+    assert torch.equal(idx[sure].long(), want[sure, :k])
+    w64 = torch.softmax(val[:, :k], 1)
+    # one rounding of each logit's distance from the largest, exp, sum and division
+    spread = val[:, :1] - val[:, k - 1:k]
+    assert ((w.double() - w64).abs() <= w64 * (E32 * (64 + 2 * spread) + 4 * d * E64 * mag)).all()
+
+
 @pytest.mark.parametrize("t", [1, 40])
 @pytest.mark.parametrize("e", [2, 3, 9, 17, 250])
 def test_moe_equal_experts_tie(t, e):
