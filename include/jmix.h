@@ -354,7 +354,8 @@ jm_status jm_norm_bwd(const jm_norm_dims* dims, const void* g_y, const void* x,
                       void* g_weight, void* g_bias, void* workspace, size_t ws_bytes,
                       jm_stream_t stream);
 
-/* Activation of jm_linear_fwd: GELU is v Phi(v) (the exact, erf form). */
+/* Activation of jm_linear_fwd: GELU is v Phi(v) (the erf form; within 2^-16 of its value,
+ * before rounding, down to v = -12). */
 enum { JM_ACT_NONE = 0, JM_ACT_RELU = 1, JM_ACT_GELU = 2, JM_ACT_SILU = 3 };
 
 typedef struct {

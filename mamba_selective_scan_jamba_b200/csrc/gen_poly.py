@@ -1,5 +1,5 @@
-"""Derives the polynomial constants of the scan kernel's FMA-pipe functions and
-writes csrc/poly_consts.cuh.
+"""Derives the polynomial constants of the scan kernel's FMA-pipe functions and of the
+normal distribution's tail, and writes csrc/poly_consts.cuh.
 
 * exp2(f) on f in [-1/2, 1/2]: degree-6 minimax polynomial in the relative
   error (Remez exchange algorithm).  Used with the exact base-2 range
@@ -10,6 +10,11 @@ writes csrc/poly_consts.cuh.
 * 1/x: Newton-Raphson r <- r (2 - x r) from the bit-pattern initial guess
   r0 = as_float(K - bits(x)); K is chosen here to minimise the largest
   relative error of r0 over one binade (the error pattern repeats per binade).
+
+* Phi(-a) exp(a^2 / 2) for a in [0, 14], the normal tail without its exponential:
+  t * P(t), t = 1 / (1 + NC a), P of degree 7, minimax in the relative error (1.7e-7).
+  The function is the integral of exp(-a s - s^2 / 2) over s >= 0, divided by
+  sqrt(2 pi).
 
 The polynomials are fitted in float64 and stored as float32; the float32
 evaluation error bounds are checked by tests/test_poly_consts.py.
@@ -68,8 +73,24 @@ def rcp_magic() -> int:
     return min(range(best - 0x100, best + 0x101), key=err)
 
 
+TAIL_C = 0.3
+
+
+def tail_over_t(t):
+    t = np.asarray(t, dtype=np.float64)
+    a = ((1.0 / t - 1.0) / TAIL_C).reshape(-1, 1)
+    x, w = np.polynomial.legendre.leggauss(96)
+    s, w = 4.5 * (x + 1.0), 4.5 * w          # (behind 9 the integrand is below 1e-17)
+    r = np.exp(-a * s - 0.5 * s * s) @ w / np.sqrt(2.0 * np.pi)
+    return r.reshape(t.shape) / t
+
+
+def tail_coeffs():
+    return remez(tail_over_t, 7, 1.0 / (1.0 + 14.0 * TAIL_C), 1.0, grid=4001).astype(np.float32)
+
+
 def render() -> str:
-    e, l = exp2_coeffs(), log1p_coeffs()
+    e, l, n = exp2_coeffs(), log1p_coeffs(), tail_coeffs()
     fmt = lambda v: "%.9ef" % float(v)
     out = ["// Generated by gen_poly.py: minimax polynomials (Remez exchange) in float32.",
            "#pragma once", "", "namespace jmix {", "namespace poly {", "",
@@ -77,6 +98,9 @@ def render() -> str:
     out += ["constexpr float E%d = %s;" % (i, fmt(v)) for i, v in enumerate(e)]
     out += ["", "// log1p(w) ~ w*(L0 + w*(L1 + ...)) for w in [0, 1]"]
     out += ["constexpr float L%d = %s;" % (i, fmt(v)) for i, v in enumerate(l)]
+    out += ["", "// Phi(-a) exp(a^2 / 2) ~ t*(N0 + t*(N1 + ...)), t = 1 / (1 + NC a), for a in [0, 14]",
+            "constexpr float NC = %s;" % fmt(TAIL_C)]
+    out += ["constexpr float N%d = %s;" % (i, fmt(v)) for i, v in enumerate(n)]
     out += ["", "// 1/x initial guess: as_float(RCP_MAGIC - bits(x)), then Newton-Raphson",
             "constexpr int RCP_MAGIC = 0x%x;" % rcp_magic()]
     out += ["", "}  // namespace poly", "}  // namespace jmix", ""]

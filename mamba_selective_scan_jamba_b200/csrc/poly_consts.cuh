@@ -24,6 +24,17 @@ constexpr float L6 = 7.822595537e-02f;
 constexpr float L7 = -2.950523980e-02f;
 constexpr float L8 = 5.232694093e-03f;
 
+// Phi(-a) exp(a^2 / 2) ~ t*(N0 + t*(N1 + ...)), t = 1 / (1 + NC a), for a in [0, 14]
+constexpr float NC = 3.000000000e-01f;
+constexpr float N0 = 1.196293011e-01f;
+constexpr float N1 = 1.207539588e-01f;
+constexpr float N2 = 9.991349280e-02f;
+constexpr float N3 = 1.285616159e-01f;
+constexpr float N4 = -5.368361995e-02f;
+constexpr float N5 = 2.063534856e-01f;
+constexpr float N6 = -1.572030634e-01f;
+constexpr float N7 = 3.567476943e-02f;
+
 // 1/x initial guess: as_float(RCP_MAGIC - bits(x)), then Newton-Raphson
 constexpr int RCP_MAGIC = 0x7ef311c2;
 

@@ -328,3 +328,28 @@ def test_linear_pairs_end_with_every_signal_received(m, k, n):
         assert jmix.jm_poll_error(ws) == jmix.JM_OK, jmix.jm_last_error()
     for q in outs:
         assert torch.equal(q[0], out) and torch.equal(q[1], o["g_x"]) and torch.equal(q[2], o["g_w"])
+
+
+@pytest.mark.parametrize("m", [16, 700])
+def test_linear_gelu_tail(m):
+    """GELU and its derivative keep their relative accuracy far below zero, where they are the
+    normal tail: float32 values of up to 12 squared and halved carry 72 * 2 roundings into the
+    exponential, 2^-16 in all, then one rounding to bf16.  The derivative is the difference
+    of the two terms that the bound adds.  (The reference's tail by erfc: torch's ndtr is 0
+    below -8.3 on a GPU.)"""
+    import torch
+    v = -torch.exp2(torch.linspace(-6, 3.58, 8 * m, dtype=torch.float64))   # to -11.96
+    x = v.to(torch.bfloat16).cuda().view(m, 8)
+    eye = torch.eye(8, device="cuda", dtype=torch.bfloat16)
+    t = dict(x=x, w=eye, b=torch.zeros(8, device="cuda", dtype=torch.bfloat16),
+             r=torch.zeros_like(x), g=torch.ones_like(x))
+    out, pre = run_fwd(t, "gelu", bias=False, residual=False)
+    assert torch.equal(pre, x)
+    p = x.double()
+    phi = 0.5 * torch.special.erfc(-p / 2 ** 0.5)
+    ref = p * phi
+    assert ((out.double() - ref).abs() <= (HALF + 2.0 ** -16) * ref.abs()).all()
+    gx = run_bwd(t, "gelu", pre, ("g_x",))["g_x"].double()
+    dens = p.abs() * torch.exp(-p * p / 2) / (2 * torch.pi) ** 0.5
+    tol = HALF * (phi - dens).abs() + 2.0 ** -16 * (phi + dens)
+    assert ((gx - (phi - dens)).abs() <= tol).all()

@@ -60,6 +60,22 @@ def test_log1p_polynomial():
     assert (np.abs(val[ok] - ref[ok]) / ref[ok]).max() < 3e-7
 
 
+def test_normal_tail_polynomial():
+    """t P(t) in float32 against the tail by erfc: 1.7e-7 of the polynomial and 7 roundings."""
+    import math
+    c = header_consts()
+    N = [c["N%d" % i] for i in range(8)]
+    a = np.concatenate([np.linspace(0, 14, 4001), np.geomspace(1e-6, 14, 2001)]).astype(np.float32)
+    t = (np.float32(1) / (np.float32(1) + c["NC"] * a)).astype(np.float32)
+    p = np.float32(N[7])
+    for k in range(6, -1, -1):
+        p = (p * t + N[k]).astype(np.float32)
+    val = (p * t).astype(np.float64)
+    a64 = a.astype(np.float64)
+    ref = np.array([0.5 * math.erfc(v / math.sqrt(2)) for v in a64]) * np.exp(a64 * a64 / 2)
+    assert (np.abs(val - ref) / ref).max() < 1.7e-7 + 7 * 2.0 ** -23
+
+
 def test_newton_reciprocal():
     c = header_consts_int()
     K = c["RCP_MAGIC"]
