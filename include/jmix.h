@@ -421,8 +421,9 @@ typedef struct {
  *   router_w  in:  [E, D];  w_gate, w_up in: [E, F, D];  w_down in: [E, D, F]
  *   out       out: [tokens, D]
  *   topk_idx  out: int32 [tokens, K], e_i, or NULL;  topk_w out: float32 [tokens, K] or NULL
- * Logits are summed in float64, products in float32; out is rounded once.  Sums have a
- * fixed order: two runs give the same bits.  Only the chosen experts' weights are read.
+ * Logits are float64 sums of products that float32 holds exactly (inside its range); the
+ * experts' products are float32 sums; out is rounded once.  Sums have a fixed order: two runs
+ * give the same bits.  Only the chosen experts' weights are read.
  * Any other overlap of an output with an input or another output is refused.  Workspace:
  * jm_moe_fwd_workspace_size(dims) bytes, 256-byte aligned; its first 256 bytes are the
  * error header jm_poll_error reads.  The second kernel is launched cooperatively, one
