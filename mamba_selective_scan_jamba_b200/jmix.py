@@ -290,15 +290,16 @@ def jm_scan_bwd(d: jm_dims, delta, u, Bm, Cm, A_log, D, h0, gy, g_delta, g_u, g_
 # stride in the dims, or bytes of any type.
 _IO, _F32, _I32, _ROWS, _RAW = range(5)
 _types = None      # torch dtypes by kind for JM_F32 and JM_BF16, once torch is imported
-_raw_stream = None
+_raw_stream = _raw_device = None   # of a program with a CUDA tensor (CUDA is set up)
 
 
 def _use_torch() -> None:
-    global _types, _raw_stream
+    global _types, _raw_stream, _raw_device
     import torch
     f, i, b = torch.float32, torch.int32, torch.bfloat16
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _types = {JM_F32: (f, f, i, f), JM_BF16: (b, f, i, b)}
 
 
@@ -306,15 +307,19 @@ def _bad(msg: str):
     raise JmixError(JM_ERR_INVALID_ARG, msg)
 
 
+def _too_few(name, kind, t, need):
+    has, of = (t.nbytes, "bytes") if kind == _RAW else (t.numel(), "values")
+    _bad(f"{name} has {has} {of}, the call needs {need}")
+
+
 def _check_rows(name, t, d) -> None:
     """The rows of t, all dimensions but the last, have to lie d.x_stride values apart: a 3-D
-    slice or a transposed tensor has no such pitch, and its address does not say so.  (Where
-    t and the dims' rows are both packed, t may be grouped otherwise; a tensor of one
-    dimension is memory without rows of its own.)"""
-    if t.is_contiguous() and (d.x_stride == d.cols or t.dim() < 2):
+    slice or a transposed tensor has no such pitch, and its address does not say so.  (A
+    contiguous tensor of one dimension is memory without rows of its own.)"""
+    if t.dim() < 2 and t.is_contiguous():
         need = (d.rows - 1) * d.x_stride + d.cols if d.rows > 0 else 0
         if t.numel() < need:
-            _bad(f"{name} has {t.numel()} values, the call needs {need}")
+            _too_few(name, _ROWS, t, need)
         return
     if t.dim() < 2 or t.shape[-1] > 1 and t.stride(-1) != 1:
         _bad(f"{name} is not contiguous")
@@ -338,7 +343,8 @@ def _call(fn, d, spec, needs, tensors, tail=(), stream=None, check: bool = True)
     """fn(d, addresses of `tensors`, *tail, stream).  A tensor's layout, type, size and device
     cannot be read from its address, so they are checked here against `spec`, a tuple of
     (name, kind), and `needs`, the values (of the workspace: bytes) the call reads or writes
-    there.  (A decode step's operators take microseconds: this path is kept short.)"""
+    there, None for x with rows that are not packed.  (A decode step's operators take
+    microseconds: this path is kept short.)"""
     if _types is None:
         _use_torch()
     types, dev, args = _types.get(d.io, _types[JM_BF16]), -1, []
@@ -348,18 +354,16 @@ def _call(fn, d, spec, needs, tensors, tail=(), stream=None, check: bool = True)
             continue
         if kind != _RAW and t.dtype is not types[kind]:
             _bad(f"{name} is {t.dtype}, the call needs {types[kind]}")
-        if kind == _ROWS:
+        if need is None or not t.is_contiguous():
+            if kind != _ROWS:
+                _bad(f"{name} is not contiguous")
             _check_rows(name, t, d)
-        elif not t.is_contiguous():
-            _bad(f"{name} is not contiguous")
-        has = t.nbytes if kind == _RAW else t.numel()
-        if has < need:
-            _bad(f"{name} has {has} {'bytes' if kind == _RAW else 'values'}, the call needs {need}")
+        elif (t.numel() if kind != _RAW else t.nbytes) < need:
+            _too_few(name, kind, t, need)
         at = t.get_device()
         if at != dev or at < 0:
             if at >= 0 and dev < 0:
-                import torch
-                dev = torch.cuda.current_device()
+                dev = _raw_device()
             if at != dev or at < 0:
                 _bad(f"{name} is on {t.device}, not on the current CUDA device")
         args.append(t.data_ptr())
@@ -394,7 +398,8 @@ def jm_norm_fwd(d: jm_norm_dims, x, weight, y, bias=None, residual=None, sum_out
     """Residual add and LayerNorm / RMSNorm of each row (see include/jmix.h)."""
     rows, c = d.rows, d.cols
     n = rows * c
-    return _call(load().jm_norm_fwd, d, _NORM_FWD, (n, n, c, c, n, n, 2 * rows),
+    return _call(load().jm_norm_fwd, d, _NORM_FWD,
+                 (n if d.x_stride == c else None, n, c, c, n, n, 2 * rows),
                  (x, residual, weight, bias, y, sum_out, stats), (), stream, check)
 
 
@@ -407,7 +412,8 @@ def jm_norm_bwd(d: jm_norm_dims, g_y, x, weight, stats, g_x, workspace, ws_bytes
     """Backward of jm_norm_fwd (see include/jmix.h); x is the forward's sum, or its x."""
     rows, c = d.rows, d.cols
     n = rows * c
-    return _call(load().jm_norm_bwd, d, _NORM_BWD, (n, n, c, 2 * rows, n, n, c, c, ws_bytes),
+    return _call(load().jm_norm_bwd, d, _NORM_BWD,
+                 (n, n if d.x_stride == c else None, c, 2 * rows, n, n, c, c, ws_bytes),
                  (g_y, x, weight, stats, g_sum, g_x, g_weight, g_bias, workspace), (ws_bytes,),
                  stream, check)
 
