@@ -347,7 +347,8 @@ jm_status jm_norm_fwd(const jm_norm_dims* dims, const void* x, const void* resid
  *   g_weight, g_bias out: [cols], each may be NULL; g_bias must be NULL for JM_NORM_RMS
  * Sums are float32 in a fixed order: two runs give the same bits.  Workspace:
  * jm_norm_bwd_workspace_size(dims) bytes, 256-byte aligned; its first 256 bytes
- * are the error header jm_poll_error reads.  dims->eps is not read. */
+ * are the error header jm_poll_error reads.  dims->eps is checked as for jm_norm_fwd, and
+ * not used (stats hold rstd). */
 size_t jm_norm_bwd_workspace_size(const jm_norm_dims* dims);
 jm_status jm_norm_bwd(const jm_norm_dims* dims, const void* g_y, const void* x,
                       const void* weight, const float* stats, const void* g_sum, void* g_x,

@@ -293,8 +293,11 @@ JM_API jm_status jm_linear_fwd(const jm_linear_dims* dims, const void* x, const 
                N = (size_t)dims->out_features;
   const bool any = M > 0;
   const size_t need = jm_linear_fwd_workspace_size(dims);
-  // the residual is checked apart: it may be exactly out's buffer (each value is read
-  // by the thread that then writes it)
+  // the residual is checked apart: it may be exactly out's buffer, since every value of it is
+  // read before out is written there: by the same thread in the few-row kernel and the sum of
+  // K splits; in the pairs' kernel box by box, where a residual box and an output box are the
+  // same 64 columns x 128 rows of one epilogue group and the load has landed before the store
+  // is issued
   const Arg in[] = {{"x", x, M * K * 2, any},
                     {"w", w, N * K * 2, true},
                     {"bias", bias, N * 2, false},

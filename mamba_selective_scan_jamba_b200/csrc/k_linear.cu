@@ -174,7 +174,8 @@ struct Drain {
     return smem_u32(stage + b * kOutBytes);
   }
 
-  // A buffer for the next chunk (with pre, which goes out first, both), and its residual.
+  // A buffer for the next chunk (with pre, which goes out first, both), and its residual: the
+  // box that finish() stores to, and no other, since out may be the residual's buffer.
   __device__ __forceinline__ void open(const CUtensorMap& tm_res, int64_t col, int64_t row0) {
     if (first) {
       if (g.ep.pre)
@@ -641,9 +642,10 @@ struct Cut {
   int bn, cpairs, splits;
 };
 
-// Estimated microseconds: waves of work items on 74 pairs (a 64-wide chunk of a 256 x
-// 256 tile takes a pair 0.28 us, of a 256 x 128 tile 0.16); 1 us for a cluster's
-// exchange; for splits the partial tiles' round trip through L2 and one launch.  Measured:
+// Estimated microseconds, without the start and the end that every cut has alike (some 5 us):
+// waves of work items on 74 pairs (a 64-wide chunk of a 256 x 256 tile takes a pair 0.28 us, of a
+// 256 x 128 tile 0.16); 1 us for a cluster's exchange; for splits the partial tiles' round trip
+// through L2 and one launch.  Each product is cut by itself.  Measured:
 // 256 x 8192 x 4096 two pairs 20 us, two splits 23; 530 x 5496 x 2208 one wave of two pairs a
 // 256 x 256 tile 23.5 us, of uncut 256 x 128 tiles 28.7; 600 x 2048 x 512 two pairs
 // 7.3 us, 4 splits 8.0, uncut 9.2.  (Tiles of 4 pairs took 6 us more than their splits.)

@@ -309,9 +309,9 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& x, const FewArgs
 
 }  // namespace
 
-// Up to 64 rows, and up to 192 over a long contracted index: a tile's exchange grows with the
-// rows, k_linear_pair's does not, but its 256-row tiles read the weights no faster for few
-// rows.  Microseconds here and there: 96 rows, 512 -> 4096 6.2, 5.5; 1024 -> 4096 7.0, 7.2;
+// Up to 64 rows, and up to 192 over a long contracted index, whatever the number of features
+// (measured with 1024 to 8192): a tile's exchange grows with the rows, k_linear_pair's does not,
+// but its 256-row tiles read the weights no faster for few rows.  Microseconds here and there: 96 rows, 512 -> 4096 6.2, 5.5; 1024 -> 4096 7.0, 7.2;
 // 128 rows, 1024 -> 1024 6.6, 6.2; 8192 -> 4096 15.8, 19.2; 160 rows, 2048 -> 4096 9.3, 8.9;
 // 4096 -> 8192 17.5, 20.1; 192 rows, 4096 -> 1024 10.4, 9.1; 8192 -> 4096 18.5, 19.6; 256
 // rows, 8192 -> 4096 21.9, 19.8.

@@ -5,15 +5,19 @@
 //   out = sum_i g_i h_i Wdown_{e_i}^T + residual
 //
 // k_moe_route: one CTA, or with few tokens a cluster, per token; logits, choice, weights.
-// k_moe: one CTA per SM streams the chosen experts' weights once.  With few tokens
+// k_moe: one CTA per SM streams the chosen experts' weights, once for each block of an
+// expert's tokens (moe_block: 16 to 128 rows, twice an even router's share).  With few tokens
 // those bytes bound the layer (an expert of 4096 x 14336 is 352 MB: 54 us of HBM time,
 // its products for 32 tokens 7 us of tensor time), so the design keeps HBM busy:
 //
 // * The weights are the MMA's A operand (128 rows of weights = TMEM lanes), the tokens
-//   its N: few tokens waste tensor time that is free here, and no weight is read twice.
+//   its N: few tokens waste tensor time that is free here, and no weight is read twice for a
+//   block.  An expert that gets more rows than one block holds is streamed again for the next
+//   one.  256 tokens of 4096, floors behind the times: one expert of 14336, two blocks, 127 us,
+//   54; 16 experts, top 2, the same two chosen by every token, four blocks each, 354 us, 107.
 // * A phase's work is a line of units (block of an expert's tokens, tile of weight rows)
 //   x K steps of 64, cut into equal contiguous ranges, one per CTA: every SM streams the
-//   same bytes whatever the number of experts in use.  A step brings 256 weight rows:
+//   same bytes whatever the number of blocks.  A step brings 256 weight rows:
 //   128 of gate and the same 128 of up in the first phase (so that h is formed in the
 //   thread that holds both), 256 of down in the second.
 // * A unit inside one CTA's range is finished from TMEM.  A cut one leaves float32

@@ -228,6 +228,8 @@ def test_moe_two_calls_on_two_streams():
         assert jmix.jm_poll_error(w) == jmix.JM_OK
 
 
+# Logits are float64 sums of exact products: within d + 16 roundings of E64 of sum|x w|.  (The
+# bound of 16 eps32 at the top of this file was for sums of 8 of them in float32; it holds.)
 E64 = 2.0 ** -53
 
 
